@@ -239,6 +239,40 @@ mla_status mla_prefill_attn(const mla_bf16* q_full, const mla_bf16* cache, const
                             mla_bf16* out_lat, float* lse, void* stream);
 
 /*
+ * (3-window) Attention with a sliding window and sinks over the latent cache (the pages have no
+ *     counterpart; the attention of (3) with a mask): a query row of cached length L attends to
+ *         V(L) = { t < L : t < sinks  or  t >= L - window }
+ *     i.e. to the first `sinks` tokens and the last `window` ones.  The tokens between them are not
+ *     read (but for those that share a 64-token box with visible ones; whatever those hold, infinities
+ *     and NaN included, has no effect).  Keys keep the rotation of the position they were appended at.
+ * window >= 0 and sinks >= 0, else MLA_ERR_INVALID_ARG; either may exceed the sequence.  window == 0
+ * leaves the sinks alone, window == sinks == 0 leaves every row empty: out_lat = 0, lse = -inf, as
+ * does a length of 0.  A row with L <= sinks + window attends to all of its tokens.
+ * mla_decode_attn_window(_fp8): the arguments of mla_decode_attn(_fp8); row b reads sequence b.
+ * mla_prefill_attn_window: those of mla_prefill_attn; row i reads sequence q_seq[i] with L = q_len[i].
+ *   workspace >= mla_decode_workspace_size(rows, mla_window_span(capacity, window, sinks), num_splits)
+ *   bytes, capacity = max_seq_len or max_blocks_per_seq * 64 (the size for the full capacity also serves)
+ * Work ranges are planned over the visible boxes only; results do not depend on the cache layout.
+ */
+mla_status mla_decode_attn_window(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                                  const int32_t* seq_lens, mla_cache_desc desc, int32_t batch, int32_t window,
+                                  int32_t sinks, float softmax_scale, int32_t num_splits, void* workspace,
+                                  size_t workspace_bytes, mla_bf16* out_lat, float* lse, void* stream);
+mla_status mla_decode_attn_window_fp8(const mla_bf16* q_full, const uint8_t* cache, const uint8_t* scales,
+                                      const int32_t* block_table, const int32_t* seq_lens, mla_cache_desc desc,
+                                      int32_t batch, int32_t window, int32_t sinks, float softmax_scale,
+                                      int32_t num_splits, void* workspace, size_t workspace_bytes, mla_bf16* out_lat,
+                                      float* lse, void* stream);
+mla_status mla_prefill_attn_window(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                                   const int32_t* q_seq, const int32_t* q_len, mla_cache_desc desc, int32_t n_queries,
+                                   int32_t window, int32_t sinks, float softmax_scale, int32_t num_splits,
+                                   void* workspace, size_t workspace_bytes, mla_bf16* out_lat, float* lse,
+                                   void* stream);
+/* The most cached tokens (whole 64-token boxes) such a row reads when its sequence holds up to
+ * max_seq_len; 0 for a negative argument. */
+int32_t mla_window_span(int32_t max_seq_len, int32_t window, int32_t sinks);
+
+/*
  * (3-fp8) Decode attention over an FP8 latent cache — [DR] §4.2 效率证据 (FP8 KV cache) with the
  *     attention of (3): every cached row is taken as code_value * 2^(scales[row] - 127), the rows
  *     mla_cache_append_fp8 writes, and attended exactly as mla_decode_attn attends bf16 rows (the

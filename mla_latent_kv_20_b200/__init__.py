@@ -62,6 +62,12 @@ def _load():
         "mla_decode_workspace_size": (SZ, [I32, I32, I32]),
         "mla_decode_attn": (ctypes.c_int, [P, P, P, P, CacheDesc, I32, F32, I32, P, SZ, P, P, P]),
         "mla_prefill_attn": (ctypes.c_int, [P, P, P, P, P, CacheDesc, I32, F32, I32, P, SZ, P, P, P]),
+        "mla_decode_attn_window": (ctypes.c_int, [P, P, P, P, CacheDesc, I32, I32, I32, F32, I32, P, SZ, P, P, P]),
+        "mla_decode_attn_window_fp8": (ctypes.c_int,
+                                       [P, P, P, P, P, CacheDesc, I32, I32, I32, F32, I32, P, SZ, P, P, P]),
+        "mla_prefill_attn_window": (ctypes.c_int,
+                                    [P, P, P, P, P, CacheDesc, I32, I32, I32, F32, I32, P, SZ, P, P, P]),
+        "mla_window_span": (I32, [I32, I32, I32]),
         "mla_unabsorb_v": (ctypes.c_int, [P, P, P, I32, P]),
         "mla_decode_attn_noalloc": (ctypes.c_int, [P, P, P, P, CacheDesc, I32, F32, I32, P, P, P]),
         "mla_noalloc_scratch_bytes": (SZ, []),
@@ -190,6 +196,48 @@ def prefill_attn(q_full, cache, q_seq, q_len, desc: CacheDesc, workspace, out_la
     _check(lib.mla_prefill_attn(_ptr(q_full), _ptr(cache), _ptr(block_table), _ptr(q_seq), _ptr(q_len), desc, n,
                                 softmax_scale, num_splits, _ptr(workspace), wb, _ptr(out_lat), _ptr(lse),
                                 _stream(stream)), "mla_prefill_attn")
+
+
+def window_span(max_seq_len: int, window: int, sinks: int = 0) -> int:
+    """Cached tokens a windowed row reads at most; sizes the workspace of the windowed calls
+    (decode_workspace_size(rows, window_span(capacity, window, sinks), num_splits))."""
+    return lib.mla_window_span(max_seq_len, window, sinks)
+
+
+def decode_attn_window(q_full, cache, seq_lens, desc: CacheDesc, workspace, out_lat, *, window: int, sinks: int = 0,
+                       lse=None, block_table=None, softmax_scale: float = 1.0 / 192 ** 0.5, num_splits: int = 0,
+                       stream=None, batch: int | None = None, workspace_bytes: int | None = None):
+    """mla_decode_attn_window: row b attends to the first `sinks` and the last `window` tokens of sequence b."""
+    b = q_full.shape[0] if batch is None else batch
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(lib.mla_decode_attn_window(_ptr(q_full), _ptr(cache), _ptr(block_table), _ptr(seq_lens), desc, b, window,
+                                      sinks, softmax_scale, num_splits, _ptr(workspace), wb, _ptr(out_lat), _ptr(lse),
+                                      _stream(stream)), "mla_decode_attn_window")
+
+
+def decode_attn_window_fp8(q_full, cache, scales, seq_lens, desc: CacheDesc, workspace, out_lat, *, window: int,
+                           sinks: int = 0, lse=None, block_table=None, softmax_scale: float = 1.0 / 192 ** 0.5,
+                           num_splits: int = 0, stream=None, batch: int | None = None,
+                           workspace_bytes: int | None = None):
+    """mla_decode_attn_window_fp8: the windowed decode over an FP8 cache."""
+    b = q_full.shape[0] if batch is None else batch
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(lib.mla_decode_attn_window_fp8(_ptr(q_full), _ptr(cache), _ptr(scales), _ptr(block_table), _ptr(seq_lens),
+                                          desc, b, window, sinks, softmax_scale, num_splits, _ptr(workspace), wb,
+                                          _ptr(out_lat), _ptr(lse), _stream(stream)), "mla_decode_attn_window_fp8")
+
+
+def prefill_attn_window(q_full, cache, q_seq, q_len, desc: CacheDesc, workspace, out_lat, *, window: int,
+                        sinks: int = 0, lse=None, block_table=None, softmax_scale: float = 1.0 / 192 ** 0.5,
+                        num_splits: int = 0, stream=None, n_queries: int | None = None,
+                        workspace_bytes: int | None = None):
+    """mla_prefill_attn_window: query row i attends to the first `sinks` and the last `window` of the
+    first q_len[i] tokens of sequence q_seq[i]."""
+    n = q_full.shape[0] if n_queries is None else n_queries
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(lib.mla_prefill_attn_window(_ptr(q_full), _ptr(cache), _ptr(block_table), _ptr(q_seq), _ptr(q_len), desc, n,
+                                       window, sinks, softmax_scale, num_splits, _ptr(workspace), wb, _ptr(out_lat),
+                                       _ptr(lse), _stream(stream)), "mla_prefill_attn_window")
 
 
 NOALLOC_SCRATCH_BYTES = int(lib.mla_noalloc_scratch_bytes())   # the library's own constant

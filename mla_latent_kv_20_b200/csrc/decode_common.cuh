@@ -32,6 +32,8 @@
 
 #include <cuda_bf16.h>
 
+#include <climits>
+
 #include "append.cuh"
 
 namespace mla {
@@ -84,6 +86,50 @@ __device__ __forceinline__ int seq_len_checked(const int32_t* seq_lens, int b, i
 }
 __host__ __device__ __forceinline__ int tiles_of(int L) { return (L + kTile - 1) / kTile; }
 
+// What a query row of cached length L attends to.
+//
+// FullRows: every token t < L.
+//
+// WindowRows (sliding window with sinks): the first `sinks` tokens and the last `window` ones,
+//   V(L) = { t < L : t < sinks or t >= L - window };
+// the tokens between them are neither copied nor scored.  The plan, the ranges and the segments
+// count a row's tokens in a shortened frame: the whole 64-token boxes that hold a visible token, laid
+// end to end, so frame token v stands for token v below `first` (the sinks' boxes) and v + shift
+// from there on, shift a multiple of 64.  A box never crosses a page, the same boxes are used in
+// paged and contiguous caches, and every box holds a visible token.  Hidden tokens that share a box
+// with visible ones, [hole0, hole1), get a score of -inf and a zeroed V row (0 * inf would be NaN).
+struct FullRows {
+  static constexpr bool kHoles = false;
+  struct Map {
+    __device__ __forceinline__ int real(int v) const { return v; }
+    __device__ __forceinline__ bool in_sinks(int) const { return false; }
+    __device__ __forceinline__ int hole0() const { return 0; }
+    __device__ __forceinline__ int hole1() const { return 0; }
+  };
+  __device__ __forceinline__ int span(int L) const { return L; }
+  __device__ __forceinline__ Map map(int) const { return {}; }
+};
+struct WindowRows {
+  static constexpr bool kHoles = true;
+  int window, sinks;
+  struct Map {
+    int first, shift, h0, h1;
+    __device__ __forceinline__ int real(int v) const { return v < first ? v : v + shift; }
+    __device__ __forceinline__ bool in_sinks(int v) const { return v < first; }
+    __device__ __forceinline__ int hole0() const { return h0; }
+    __device__ __forceinline__ int hole1() const { return h1; }
+  };
+  // Without a window only the sinks are left: a row of at most `sinks` tokens.
+  __device__ __forceinline__ int visible_end(int L) const { return window > 0 ? L : min(L, sinks); }
+  __device__ __forceinline__ Map map(int L) const {
+    const int start = max(visible_end(L) - window, 0);
+    if (start <= sinks) return {INT_MAX, 0, 0, 0};   // no gap
+    const int first = (sinks + 63) & ~63;
+    return {first, max((start & ~63) - first, 0), sinks, start};
+  }
+  __device__ __forceinline__ int span(int L) const { return visible_end(L) - map(L).shift; }
+};
+
 // floor(x y / z) for x, y >= 0 and z > 0, exact; 32-bit arithmetic when x y fits (the wide
 // division is out of line: it is rarely taken and its code is long).
 __host__ __device__ __noinline__ int muldiv_wide(uint64_t p, uint32_t z) { return static_cast<int>(p / z); }
@@ -112,6 +158,7 @@ struct Segment {
   int n_tiles;
   bool direct;   // covers the whole sequence: the decode kernel writes the final output
   int slot;      // workspace slot of the partial otherwise
+  int len;       // cached tokens of the sequence ([tok_begin, tok_end) is in the frame of Rows)
 };
 
 // Walks the segments of one work range in order.  Every role of a CTA walks the same sequence.
@@ -128,9 +175,11 @@ struct SegmentCursor {
   // False only if next() will return false (true may still be followed by no segment).
   __device__ bool may_continue() const { return b < b_end && off < end; }
 
-  __device__ bool next(const int32_t* seq_lens, int capacity, Segment& s) {
+  template <class Rows>
+  __device__ bool next(const int32_t* seq_lens, int capacity, const Rows& rows, Segment& s) {
     while (b < b_end && off < end) {
-      const int L = first ? len0 : seq_len_checked(seq_lens, b, capacity);
+      const int len = first ? len0 : seq_len_checked(seq_lens, b, capacity);
+      const int L = rows.span(len);
       const int tiles = tiles_of(L);
       const int t0 = (start > off ? start : off) - off;
       const int t1 = (end < off + tiles ? end : off + tiles) - off;
@@ -144,6 +193,7 @@ struct SegmentCursor {
         s.n_tiles = t1 - t0;
         s.direct = t0 == 0 && t1 == tiles;
         s.slot = first ? 2 * pair : 2 * pair + 1;
+        s.len = len;
         first = false;
         return true;
       }

@@ -113,6 +113,14 @@ int32_t mla_decode_num_splits(int32_t batch, int32_t max_seq_len, int32_t num_sp
   return p < 1 ? 1 : static_cast<int32_t>(p);
 }
 
+int32_t mla_window_span(int32_t max_seq_len, int32_t window, int32_t sinks) {
+  if (max_seq_len <= 0 || window < 0 || sinks < 0) return 0;
+  if (window == 0) return sinks < max_seq_len ? sinks : max_seq_len;
+  // the sinks' whole boxes, the window, and the hidden head of the window's first box
+  const int64_t boxes = (static_cast<int64_t>(sinks) + 63) / 64 * 64 + window + 63;
+  return boxes < max_seq_len ? static_cast<int32_t>(boxes) : max_seq_len;
+}
+
 size_t mla_decode_workspace_size(int32_t batch, int32_t max_seq_len, int32_t num_splits) {
   if (batch <= 0) return 0;
   return mla::ws_bytes(batch, mla_decode_num_splits(batch, max_seq_len, num_splits));
@@ -124,12 +132,14 @@ namespace {
 
 // The decode kernel and its combine over `rows` query rows: row b attends to the first
 // lens[b] cached tokens of sequence b, or of sequence seq_map[b] when a map is given (chunked
-// prefill).  Host checks shared by both entry points.
+// prefill); with a window, to its visible ones.  Host checks shared by the entry points.
 mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t* block_table,
                        const int32_t* lens, const int32_t* seq_map, mla_cache_desc desc, int32_t rows,
                        float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
-                       mla_bf16* out_lat, float* lse, void* stream, const uint8_t* fp8_scales = nullptr) {
+                       mla_bf16* out_lat, float* lse, void* stream, const uint8_t* fp8_scales = nullptr,
+                       const mla::WindowRows* win = nullptr) {
   const bool fp8 = fp8_scales != nullptr;
+  if (win != nullptr && (win->window < 0 || win->sinks < 0)) return MLA_ERR_INVALID_ARG;
   if (rows < 0 || num_splits < 0) return MLA_ERR_INVALID_ARG;
   if (rows > mla::kMaxDecodeBatch) return MLA_ERR_UNSUPPORTED;
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
@@ -145,7 +155,8 @@ mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t*
   if (q_full == nullptr || lens == nullptr || out_lat == nullptr) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q_full) || !aligned16(out_lat) || (lse != nullptr && !aligned16(lse))) return MLA_ERR_INVALID_ARG;
   const int capacity = cache_capacity(desc);
-  const int P = mla_decode_num_splits(rows, capacity, num_splits);
+  const int span = win != nullptr ? mla_window_span(capacity, win->window, win->sinks) : capacity;
+  const int P = mla_decode_num_splits(rows, span, num_splits);
   if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < mla::ws_bytes(rows, P))
     return MLA_ERR_WORKSPACE;
   if (desc.num_rows >= (int64_t(1) << 31) || static_cast<int64_t>(rows) * mla::kHeads >= (int64_t(1) << 31))
@@ -164,6 +175,7 @@ mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t*
   a.cache = reinterpret_cast<const uint8_t*>(cache);
   a.row_bytes = fp8 ? mla::kDRow : 2 * mla::kDRow;
   a.seq_map = seq_map;
+  a.win = win != nullptr ? *win : mla::WindowRows{0, 0};
   CUtensorMap tka, tkb, tv, tq, tsc;
   if (!make_map_slabs(&tq, q_full, static_cast<uint64_t>(rows) * mla::kHeads, 9)) return MLA_ERR_CUDA;
   if (fp8) {
@@ -180,6 +192,10 @@ mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t*
   if (fp8 && seq_map != nullptr) return MLA_ERR_UNSUPPORTED;
   auto kernel = fp8 ? mla::decode_tc_kernel<false, true>
                     : (seq_map != nullptr ? mla::decode_tc_kernel<true> : mla::decode_tc_kernel<false>);
+  if (win != nullptr)
+    kernel = fp8 ? mla::decode_tc_kernel<false, true, mla::WindowRows>
+                 : (seq_map != nullptr ? mla::decode_tc_kernel<true, false, mla::WindowRows>
+                                       : mla::decode_tc_kernel<false, false, mla::WindowRows>);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mla::kTcSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
   mla_status ls = launch_chained(kernel, dim3(2 * P), dim3(mla::tc_threads(fp8)),

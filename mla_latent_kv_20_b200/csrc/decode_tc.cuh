@@ -118,7 +118,15 @@ struct DecodeTcArgs {
   const uint8_t* cache;   // the cache buffer (L2 prefetch addresses)
   int row_bytes;          // bytes of one cached row: 1152 (bf16) or 576 (FP8 codes)
   const int32_t* seq_map; // query row -> cache sequence (chunked prefill), or null: row b reads sequence b
+  WindowRows win;         // the window and sinks (windowed instances)
 };
+template <class Rows>
+__device__ __forceinline__ Rows tc_rows(const DecodeTcArgs& a) {
+  if constexpr (Rows::kHoles)
+    return a.win;
+  else
+    return {};
+}
 
 // This CTA pair's work range, computed once per CTA at entry (the cursor's starting state).
 struct TcPlan {
@@ -245,18 +253,30 @@ __device__ __forceinline__ void tma_load_4d_local(void* dst, const CUtensorMap* 
 //        (zeros); its scores are masked anyway.
 //  V(i): per 64-token half h of the tile, latent [256n + 128r, +128) for n = 0, 1 in one box,
 //        laid out [n][chunk][64 rows][128 B].
-__device__ __forceinline__ void zero_v_rows(uint8_t* box, int v, int lane) {
+__device__ __forceinline__ void zero_v_rows(uint8_t* box, int v0, int v1, int lane) {
   // each row is 4 slabs x 128 bytes: one 16-byte chunk per lane
   uint4* p = reinterpret_cast<uint4*>(box + (lane >> 3) * kTcSlab) + (lane & 7);
-  for (int row = v; row < 64; ++row) p[row * 8] = make_uint4(0, 0, 0, 0);
+  for (int row = v0; row < v1; ++row) p[row * 8] = make_uint4(0, 0, 0, 0);
 }
 
-// A V box that reaches past the segment end: loaded through a CTA-local barrier (if any row is
-// valid), the rows past the end zeroed by all lanes after the copy has landed, then published:
-// each lane's proxy fence, the warp barrier, and lane 0's arrival with release semantics on the
-// even CTA's v_full.  Out of line: it runs at most twice per segment.  False if a wait failed.
+// Rows [h0, h1) of a 64-token box whose first token is `tok0` (in the frame of the map) that are
+// hidden behind the window.
+template <class Map>
+__device__ __forceinline__ void tc_box_hole(const Map& map, int tok0, int& h0, int& h1) {
+  const int r0 = map.real(tok0);
+  h0 = min(max(map.hole0() - r0, 0), 64);
+  h1 = min(max(map.hole1() - r0, 0), 64);
+}
+
+// A V box that reaches past the segment end, or (kHoles) holds hidden rows [h0, h1): loaded through
+// a CTA-local barrier (if any row is valid), those rows zeroed by all lanes after the copy has
+// landed, then published: each lane's proxy fence, the warp barrier, and lane 0's arrival with
+// release semantics on the even CTA's v_full.  Out of line: it runs at most twice per segment (four
+// times with a window).  False if a wait failed.
+template <bool kHoles>
 __device__ __noinline__ bool tc_load_ragged_v(uint8_t* box, const CUtensorMap* tm_v, uint64_t* fix, uint32_t fix_phase,
-                                              int row, int rank, int vcount, uint32_t vfull, volatile int* abort_flag) {
+                                              int row, int rank, int vcount, int h0, int h1, uint32_t vfull,
+                                              volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
   if (vcount > 0) {
     int ok = 1;
@@ -268,7 +288,8 @@ __device__ __noinline__ bool tc_load_ragged_v(uint8_t* box, const CUtensorMap* t
     if (__shfl_sync(0xffffffffu, ok, 0) == 0) return false;
   }
   __syncwarp();
-  zero_v_rows(box, vcount, lane);
+  if (kHoles) zero_v_rows(box, h0, h1, lane);
+  zero_v_rows(box, vcount, 64, lane);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
@@ -280,7 +301,7 @@ __device__ __noinline__ bool tc_load_ragged_v(uint8_t* box, const CUtensorMap* t
   return true;
 }
 
-template <bool kMapped, bool kFp8>
+template <bool kMapped, bool kFp8, class Rows>
 __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, const CUtensorMap* tm_v,
                             const CUtensorMap* tm_q, const CUtensorMap* tm_sc, const DecodeTcArgs& a,
                             const TcPlan& plan, uint8_t* smem, TcBars* bars, uint32_t rank, int pair,
@@ -301,9 +322,11 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
   int k = 0;    // segment index
   uint32_t fix_phase = 0;
   bool ok = true;
-  PageWindow pw;
+  PageWindow pw, pw_sinks;   // the sinks' pages have ids of their own: tile 0 looks up both places
   const bool paged = a.v.page_size != 0;
-  while (ok && cur.next(a.seq_lens, a.capacity, sg)) {
+  const Rows rows = tc_rows<Rows>(a);
+  while (ok && cur.next(a.seq_lens, a.capacity, rows, sg)) {
+    const auto map = rows.map(sg.len);
     const int b = sg.b, t_begin = sg.tok_begin, t_end = sg.tok_end, n_tiles = sg.n_tiles;
     // Q of sequence b.  The buffer is free once both QK^T parts have finished the previous segment.
     // Arrivals on the even CTA's barriers that only count (the data and its visibility come with
@@ -324,7 +347,9 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
     const int cb = tc_cache_seq<kMapped>(a, b, true);
     auto row_of = [&](int t) -> int {
       if (kMapped && cb < 0) return -kTcTile;
-      return paged ? pw_row(pw, a.v, cb, t, lane) : tma_row(a.v, cb, t);
+      if (!paged) return tma_row(a.v, cb, map.real(t));
+      if (Rows::kHoles && map.in_sinks(t)) return pw_row(pw_sinks, a.v, cb, t, lane);
+      return pw_row(pw, a.v, cb, map.real(t), lane);
     };
     auto issue_k = [&](int i) -> bool {
       const int gi = g + i;
@@ -380,7 +405,9 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
           }
           continue;
         }
-        if (vcount == 64) {
+        int h0 = 0, h1 = 0;
+        if (Rows::kHoles) tc_box_hole(map, tok0, h0, h1);
+        if (vcount == 64 && h0 == h1) {
           if (l0) {
             tma_load_4d_pair(box, tm_v, lbar(&bars->v_full[s]), 0, row, 2 * static_cast<int>(rank), 0);
             if (leader)
@@ -389,8 +416,8 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
               mbar_arrive_relaxed(lbar(&bars->v_full[s]));
           }
         } else {
-          if (!tc_load_ragged_v(box, tm_v, &bars->fix, fix_phase, row,
-                                static_cast<int>(rank), vcount, lbar(&bars->v_full[s]), abort_flag))
+          if (!tc_load_ragged_v<Rows::kHoles>(box, tm_v, &bars->fix, fix_phase, row, static_cast<int>(rank), vcount,
+                                              h0, h1, lbar(&bars->v_full[s]), abort_flag))
             return false;
           if (vcount > 0) fix_phase ^= 1u;
         }
@@ -427,15 +454,16 @@ __device__ __forceinline__ uint64_t sdesc_add(uint64_t d, uint32_t bytes) { retu
 // is reloaded for each segment.  Both issuers walk the part-A slabs (0-4) first and then part B's
 // (5-8), so part A's K slot is released halfway through the tile's QK^T (its next copy then
 // overlaps the second half and PV) and QK^T of the next tile needs part B's copy only halfway in.
+template <class Rows>
 __device__ bool tc_mma_qk(uint8_t* smem, TcBars* bars, uint32_t tmem, int j, const int32_t* seq_lens, int capacity,
-                          SegmentCursor cur, volatile int* abort_flag) {
+                          const Rows rows, SegmentCursor cur, volatile int* abort_flag) {
   const uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
   const uint64_t dq = sdesc_sw128(smem_u32(smem + kTcOffQ), 16, 1024);
   const uint64_t dk = sdesc_sw128(smem_u32(smem + kTcOffK), 16, 1024);
   const uint32_t scol = tmem + (j ? kTcColSB : kTcColSA);
   Segment sg;
   int g = 0, k = 0;
-  while (cur.next(seq_lens, capacity, sg)) {
+  while (cur.next(seq_lens, capacity, rows, sg)) {
     if (!mbar_wait_cluster(&bars->q_full, static_cast<uint32_t>(k) & 1u, 0x20)) return false;
     for (int i = 0; i < sg.n_tiles; ++i, ++g) {
       const uint32_t sb = scol + 64 * (g & 1);
@@ -470,8 +498,9 @@ __device__ bool tc_mma_qk(uint8_t* smem, TcBars* bars, uint32_t tmem, int j, con
 // accumulators); every release below therefore counts two commits.  The first V box (tokens
 // 0..63 of the tile) is consumed first so it is released (and refilled) before the second.  The
 // first tile of a segment overwrites O, after the previous segment's epilogue has read it.
+template <class Rows>
 __device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, int nh, const int32_t* seq_lens,
-                          int capacity, SegmentCursor cur, volatile int* abort_flag) {
+                          int capacity, const Rows rows, SegmentCursor cur, volatile int* abort_flag) {
   const uint32_t idesc_pv = idesc_bf16_f32(128, 256, false, true);
   const uint64_t dp = sdesc_sw128(smem_u32(smem + kTcOffP), 16, 1024);
   const uint64_t dv = sdesc_sw128(smem_u32(smem + kTcOffV + nh * 2 * kTcSlab), kTcSlab, 1024);
@@ -479,7 +508,7 @@ __device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, int nh, co
   Segment sg;
   int g = 0, k = 0;
   bool ok = true;
-  while (ok && cur.next(seq_lens, capacity, sg)) {
+  while (ok && cur.next(seq_lens, capacity, rows, sg)) {
     if (k > 0 && !mbar_wait_cluster(&bars->o_free, static_cast<uint32_t>(k - 1) & 1u, 0x25)) {
       ok = false;
       break;
@@ -551,9 +580,9 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& c, float mult, uint
 // are laid out [slab][row][64 bytes], so converter thread ct takes chunk ct + 128 j: piece ct & 3
 // of row (ct >> 2) + 32 (j & 1) of slab j >> 1.  False (the same in every converter thread) if
 // the wait failed or the kernel is aborting.
-template <int kSlabs>
-__device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, int vcount, uint64_t* raw, uint32_t parity,
-                                               uint32_t done, volatile int* abort_flag, int ct) {
+template <int kSlabs, bool kHoles>
+__device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, int vcount, int h0, int h1, uint64_t* raw,
+                                               uint32_t parity, uint32_t done, volatile int* abort_flag, int ct) {
   const bool got = mbar_wait(raw, parity, 0x17) && !*abort_flag;
   if (!named_bar_red_and(3, kTcConvThreads, got)) return false;
   const int pc = ct & 3;
@@ -569,7 +598,7 @@ __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, int 
   for (int j = 0; j < 2 * kSlabs; ++j) {
     const int row = rb + 32 * (j & 1);
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (row < vcount) e4m3x16_to_bf16(c[j], (j & 1) ? m1 : m0, lo, hi);
+    if (row < vcount && !(kHoles && row >= h0 && row < h1)) e4m3x16_to_bf16(c[j], (j & 1) ? m1 : m0, lo, hi);
     uint8_t* dst = buf + (j >> 1) * kTcSlab + row * 128;
     *reinterpret_cast<uint4*>(dst + (((2 * pc) ^ (row & 7)) << 4)) = lo;
     *reinterpret_cast<uint4*>(dst + (((2 * pc + 1) ^ (row & 7)) << 4)) = hi;
@@ -585,7 +614,7 @@ __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, int 
 
 // The converter warps walk the boxes in the producer's order: K(0), K(1), V(0), K(2), V(1), ...
 // (both parts of a K tile, then both 64-token V boxes of a tile).
-template <bool kMapped>
+template <class Rows>
 __device__ bool tc_convert(const DecodeTcArgs& a, const TcPlan& plan, int pair, uint8_t* smem, TcBars* bars,
                            volatile int* abort_flag) {
   const int ct = static_cast<int>(threadIdx.x) - 32 * kTcConvWarp0;
@@ -593,22 +622,27 @@ __device__ bool tc_convert(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   Segment sg;
   int g = 0, vn = 0;
   bool ok = true;
-  while (ok && cur.next(a.seq_lens, a.capacity, sg)) {
+  const Rows rows = tc_rows<Rows>(a);
+  while (ok && cur.next(a.seq_lens, a.capacity, rows, sg)) {
+    const auto map = rows.map(sg.len);
     const int t_begin = sg.tok_begin, t_end = sg.tok_end, n_tiles = sg.n_tiles;
     for (int i = 0; ok && i <= n_tiles; ++i) {
       if (i < n_tiles) {
         const uint32_t par = static_cast<uint32_t>(g + i) & 1u;
-        ok = tc_convert_box<kTcKSlabsA>(smem + kTcOffK, kTcFp8OffA, 64, &bars->kraw[0], par, lbar(&bars->k_full[0]),
-                                        abort_flag, ct) &&
-             tc_convert_box<kTcKSlabsB>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, 64, &bars->kraw[1], par,
-                                        lbar(&bars->k_full[1]), abort_flag, ct);
+        ok = tc_convert_box<kTcKSlabsA, false>(smem + kTcOffK, kTcFp8OffA, 64, 0, 0, &bars->kraw[0], par,
+                                               lbar(&bars->k_full[0]), abort_flag, ct) &&
+             tc_convert_box<kTcKSlabsB, false>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, 64, 0, 0,
+                                               &bars->kraw[1], par, lbar(&bars->k_full[1]), abort_flag, ct);
       }
       for (int h = 0; ok && i > 0 && h < 2; ++h, ++vn) {
         const int s = vn % kTcVSlots;
         const int tok0 = t_begin + (i - 1) * kTcTile + 64 * h;
         const int vcount = min(max(t_end - tok0, 0), 64);
-        ok = tc_convert_box<4>(smem + kTcOffV + s * kTcVBox, kTcFp8OffV, vcount, &bars->vraw[s],
-                               static_cast<uint32_t>(vn / kTcVSlots) & 1u, lbar(&bars->v_full[s]), abort_flag, ct);
+        int h0 = 0, h1 = 0;
+        if (Rows::kHoles) tc_box_hole(map, tok0, h0, h1);
+        ok = tc_convert_box<4, Rows::kHoles>(smem + kTcOffV + s * kTcVBox, kTcFp8OffV, vcount, h0, h1, &bars->vraw[s],
+                                             static_cast<uint32_t>(vn / kTcVSlots) & 1u, lbar(&bars->v_full[s]),
+                                             abort_flag, ct);
       }
     }
     g += n_tiles;
@@ -650,12 +684,12 @@ __device__ __forceinline__ void store_rows_128b(uint8_t* stage, const uint32_t (
 // still with the page rows handed over by the producer from its block-id window, so that no
 // thread waits for the block table (212 -> 225 us for the batch-128 paged workload).
 constexpr int kTcPfDist = 2;
-template <bool kMapped>
-__device__ __forceinline__ void tc_prefetch_tile(const DecodeTcArgs& a, int b, int tok0, int t_end) {
+template <bool kMapped, class Map>
+__device__ __forceinline__ void tc_prefetch_tile(const DecodeTcArgs& a, const Map& map, int b, int tok0, int t_end) {
   if (tok0 >= t_end || a.v.page_size != 0) return;
   const int cb = tc_cache_seq<kMapped>(a, b, false);   // b is the query row
   if (kMapped && cb < 0) return;
-  const int64_t r = cache_row(a.v, cb, tok0);
+  const int64_t r = cache_row(a.v, cb, map.real(tok0));
   if (r < 0) return;
   int n = min(64, t_end - tok0);
   if (a.v.num_rows - r < n) n = static_cast<int>(a.v.num_rows - r);   // rows of the buffer only
@@ -752,7 +786,7 @@ __device__ __noinline__ void tc_rescale_o(uint32_t addr, float alpha) {
   tmem_st_wait();
 }
 
-template <bool kMapped>
+template <bool kMapped, class Rows>
 __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, uint8_t* smem, TcBars* bars,
                            float* red, uint32_t tmem, uint32_t rank, volatile int* abort_flag) {
   const int warp = threadIdx.x >> 5;
@@ -768,12 +802,14 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   int g = 0;   // global tile index of the range
   int k = 0;   // segment index
   bool ok = true;
-  while (cur.next(a.seq_lens, a.capacity, sg)) {
+  const Rows rows = tc_rows<Rows>(a);
+  while (cur.next(a.seq_lens, a.capacity, rows, sg)) {
+  const auto map = rows.map(sg.len);
   const int t_begin = sg.tok_begin, t_end = sg.tok_end, n_tiles = sg.n_tiles;
   float m_used = -INFINITY;
   float l_run = 0.f;
   for (int d = 1; d < kTcPfDist && d < n_tiles; ++d)
-    tc_prefetch_tile<kMapped>(a, sg.b, t_begin + d * kTcTile + 64 * static_cast<int>(rank), t_end);
+    tc_prefetch_tile<kMapped>(a, map, sg.b, t_begin + d * kTcTile + 64 * static_cast<int>(rank), t_end);
   for (int i = 0; i < n_tiles && ok; ++i, ++g) {
     const int j = g & 1;
     if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[j], static_cast<uint32_t>(g >> 1) & 1u, 0x30))) {
@@ -804,6 +840,15 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         if (e >= nvalid) sc[e] = -INFINITY;
+    }
+    if constexpr (Rows::kHoles) {   // tokens hidden behind the window
+      const int r0 = map.real(tok0);
+      const int lo = map.hole0() - r0, hi = map.hole1() - r0;
+      if (lo < 32 && hi > 0) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e >= lo && e < hi) sc[e] = -INFINITY;
+      }
     }
     float mloc = sc[0];
 #pragma unroll
@@ -873,7 +918,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       mbar_arrive_relaxed(lbar(&bars->p_full));
     }
     if (i + kTcPfDist < n_tiles)
-      tc_prefetch_tile<kMapped>(a, sg.b, t_begin + (i + kTcPfDist) * kTcTile + 64 * static_cast<int>(rank), t_end);
+      tc_prefetch_tile<kMapped>(a, map, sg.b, t_begin + (i + kTcPfDist) * kTcTile + 64 * static_cast<int>(rank), t_end);
   }
   // ---- epilogue of the segment (every warp passes the same barriers, also after a failure)
   if (ok && !__all_sync(0xffffffffu, mbar_wait(&bars->o_final, static_cast<uint32_t>(k) & 1u, 0x33))) ok = false;
@@ -926,8 +971,9 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
 // sequences (per <= 4) the lane's lengths are loaded once, all loads in flight together, and kept
 // in registers for the three passes.
 constexpr int kTcPlanCached = 4;
-__device__ __noinline__ TcPlan tc_make_plan(const int32_t* seq_lens, int capacity, int B, int P, int32_t* table,
-                                               int pair, bool write_table) {
+template <class Rows>
+__device__ __noinline__ TcPlan tc_make_plan(const int32_t* seq_lens, int capacity, const Rows rows, int B, int P,
+                                               int32_t* table, int pair, bool write_table) {
   const int lane = threadIdx.x & 31;
   const int per = (B + 31) / 32;
   const int lo = min(B, lane * per), hi = min(B, lo + per);
@@ -949,7 +995,7 @@ __device__ __noinline__ TcPlan tc_make_plan(const int32_t* seq_lens, int capacit
   // pass 1: total tiles T, the smallest non-empty sequence, the largest, the non-empty count
   int sum = 0, mn = INT_MAX, mx = 0, nne = 0;
   for_chunk([&](int, int L) {
-    const int t = tiles_of(L);
+    const int t = tiles_of(rows.span(L));
     sum += t;
     mx = max(mx, t);
     if (t > 0) {
@@ -998,7 +1044,7 @@ __device__ __noinline__ TcPlan tc_make_plan(const int32_t* seq_lens, int capacit
   int csum = sum;
   if (per_seq) {
     csum = 0;
-    for_chunk([&](int, int L) { csum += count_of(tiles_of(L)); });
+    for_chunk([&](int, int L) { csum += count_of(tiles_of(rows.span(L))); });
   }
   const int wsum = sum + kSegCost * nne;
   int incl = csum, wincl = wsum;
@@ -1025,7 +1071,7 @@ __device__ __noinline__ TcPlan tc_make_plan(const int32_t* seq_lens, int capacit
   int run = incl - csum;
   int W = wincl - wsum;
   for_chunk([&](int bb, int L) {
-    const int t = tiles_of(L);
+    const int t = tiles_of(rows.span(L));
     const int v = count_of(t);
     if (write_table) table[bb] = per_seq ? run : W;
     if (per_seq) {
@@ -1085,8 +1131,9 @@ __device__ __noinline__ TcPlan tc_make_plan(const int32_t* seq_lens, int capacit
 // grid = 2 * P CTAs, clusters of 2 along x: blockIdx.x = 2 * pair + rank.  kMapped: query rows
 // read the cache sequences of a.seq_map (chunked prefill); the decode instance carries none of it.
 // kFp8: the cache holds E4M3 codes with E8M0 row scales (tm_ka, tm_kb, tm_v are byte maps of the
-// codes, tm_sc the 1-D byte map of the scales; unused otherwise).
-template <bool kMapped, bool kFp8 = false>
+// codes, tm_sc the 1-D byte map of the scales; unused otherwise).  Rows: what a query row attends to
+// (FullRows, or WindowRows for the sliding window with sinks).
+template <bool kMapped, bool kFp8 = false, class Rows = FullRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_ka, const __grid_constant__ CUtensorMap tm_kb,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
@@ -1157,7 +1204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
   // The producer warp computes the plan and hands it to the other warps through named barrier 2
   // (it only arrives, so its first copies need not wait for them).
   if (warp == kTcProducerWarp) {
-    const TcPlan w = tc_make_plan(a.seq_lens, a.capacity, a.batch, a.P, a.ws.off, pair, pair == 0 && rank == 0);
+    const TcPlan w = tc_make_plan(a.seq_lens, a.capacity, tc_rows<Rows>(a), a.batch, a.P, a.ws.off, pair, pair == 0 && rank == 0);
     if ((threadIdx.x & 31) == 0) *plan = w;
     __syncwarp();
     named_bar_arrive(2, tc_threads(kFp8));
@@ -1173,23 +1220,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
   if (!busy) {
     // an idle range: only the teardown below
   } else if (warp < kTcSoftmaxWarps) {
-    tc_softmax<kMapped>(a, pl, pair, smem, bars, red, tmem, rank, abort_flag);
+    tc_softmax<kMapped, Rows>(a, pl, pair, smem, bars, red, tmem, rank, abort_flag);
   } else if (warp == kTcProducerWarp) {
-    if (!tc_producer<kMapped, kFp8>(&tm_ka, &tm_kb, &tm_v, &tm_q, &tm_sc, a, pl, smem, bars, rank, pair,
+    if (!tc_producer<kMapped, kFp8, Rows>(&tm_ka, &tm_kb, &tm_v, &tm_q, &tm_sc, a, pl, smem, bars, rank, pair,
                                     abort_flag) &&
         (threadIdx.x & 31) == 0)
       *abort_flag = 1;
   } else if (kFp8 && warp >= kTcConvWarp0) {
-    if (!tc_convert<kMapped>(a, pl, pair, smem, bars, abort_flag) && threadIdx.x == 32 * kTcConvWarp0)
+    if (!tc_convert<Rows>(a, pl, pair, smem, bars, abort_flag) && threadIdx.x == 32 * kTcConvWarp0)
       *abort_flag = 1;
   } else if (rank == 0 && (threadIdx.x & 31) == 0) {
     bool ok = true;
     // One out-of-line copy of each issuer serves both of its warps (part / latent half as argument).
     const SegmentCursor cur{pl.b0, pl.off0, pl.start, pl.end, pl.b_end, pair, true, pl.len0};
     if (warp == kTcMmaWarp || warp == kTcMmaBWarp)
-      ok = tc_mma_qk(smem, bars, tmem, warp == kTcMmaWarp ? 0 : 1, a.seq_lens, a.capacity, cur, abort_flag);
+      ok = tc_mma_qk(smem, bars, tmem, warp == kTcMmaWarp ? 0 : 1, a.seq_lens, a.capacity, tc_rows<Rows>(a), cur, abort_flag);
     else
-      ok = tc_mma_pv(smem, bars, tmem, warp == kTcPvWarp ? 0 : 1, a.seq_lens, a.capacity, cur, abort_flag);
+      ok = tc_mma_pv(smem, bars, tmem, warp == kTcPvWarp ? 0 : 1, a.seq_lens, a.capacity, tc_rows<Rows>(a), cur, abort_flag);
     if (!ok) *abort_flag = 1;
   }
   __syncwarp();

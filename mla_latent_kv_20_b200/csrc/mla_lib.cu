@@ -479,6 +479,44 @@ mla_status mla_prefill_attn(const mla_bf16* q_full, const mla_bf16* cache, const
 }  // extern "C"
 
 // ------------------------------------------------------------------------------------------
+// Sliding window with sinks: the decode and prefill calls over the visible tokens of each row.
+// ------------------------------------------------------------------------------------------
+extern "C" {
+
+mla_status mla_decode_attn_window(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                                  const int32_t* seq_lens, mla_cache_desc desc, int32_t batch, int32_t window,
+                                  int32_t sinks, float softmax_scale, int32_t num_splits, void* workspace,
+                                  size_t workspace_bytes, mla_bf16* out_lat, float* lse, void* stream) {
+  const mla::WindowRows win{window, sinks};
+  return launch_attn(q_full, cache, block_table, seq_lens, nullptr, desc, batch, softmax_scale, num_splits, workspace,
+                     workspace_bytes, out_lat, lse, stream, nullptr, &win);
+}
+
+mla_status mla_decode_attn_window_fp8(const mla_bf16* q_full, const uint8_t* cache, const uint8_t* scales,
+                                      const int32_t* block_table, const int32_t* seq_lens, mla_cache_desc desc,
+                                      int32_t batch, int32_t window, int32_t sinks, float softmax_scale,
+                                      int32_t num_splits, void* workspace, size_t workspace_bytes, mla_bf16* out_lat,
+                                      float* lse, void* stream) {
+  if (scales == nullptr) return MLA_ERR_INVALID_ARG;
+  const mla::WindowRows win{window, sinks};
+  return launch_attn(q_full, cache, block_table, seq_lens, nullptr, desc, batch, softmax_scale, num_splits, workspace,
+                     workspace_bytes, out_lat, lse, stream, scales, &win);
+}
+
+mla_status mla_prefill_attn_window(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                                   const int32_t* q_seq, const int32_t* q_len, mla_cache_desc desc, int32_t n_queries,
+                                   int32_t window, int32_t sinks, float softmax_scale, int32_t num_splits,
+                                   void* workspace, size_t workspace_bytes, mla_bf16* out_lat, float* lse,
+                                   void* stream) {
+  if (n_queries > 0 && q_seq == nullptr) return MLA_ERR_INVALID_ARG;
+  const mla::WindowRows win{window, sinks};
+  return launch_attn(q_full, cache, block_table, q_len, q_seq, desc, n_queries, softmax_scale, num_splits, workspace,
+                     workspace_bytes, out_lat, lse, stream, nullptr, &win);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------
 // Decode without caller memory: split partials in a library-owned static device buffer.
 // ------------------------------------------------------------------------------------------
 namespace {

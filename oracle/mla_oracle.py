@@ -382,3 +382,52 @@ def fp8_cache_rows(c, kr_raw, pos, base: float = ROPE_BASE):
     """The FP8 cached row of a token: the row [c^KV | RoPE(k^R, pos)] (fp64 rotation, no bf16 step)
     quantized per token."""
     return quantize_rows(cache_rows(c, kr_raw, pos, base))
+
+
+# ----------------------------------------------------------------------------------------
+# Bounded latent cache (not on the pages; definitions of this library): attention with a sliding
+# window and sinks, attention weights accumulated per cached token, eviction by those weights.
+# ----------------------------------------------------------------------------------------
+def window_visible(L: int, window: int, sinks: int) -> np.ndarray:
+    """Truth values [L]: token t of a row of length L is visible if t < sinks or t >= L - window."""
+    t = np.arange(L)
+    return (t < sinks) | (t >= L - window)
+
+
+def window_rows(qf, rows, window, sinks, scale, d_latent):
+    """One query row [H, d_c + d_R] over cached rows [L, d_c + d_R], hidden tokens taken out.
+
+    Returns out_lat [H, d_c], lse [H], and what an error bound needs: pc = sum_t p_t |c_t| [H, d_c] and
+    sabs = the largest scale * sum_j |q_j row_tj| of each head [H].  No visible token: zeros and -inf."""
+    qf, rows = np.asarray(qf, np.float64), np.asarray(rows, np.float64)
+    rows = rows[window_visible(len(rows), window, sinks)]
+    H = qf.shape[0]
+    if len(rows) == 0:
+        z = np.zeros((H, d_latent))
+        return dict(out_lat=z, lse=np.full(H, -np.inf), pc=z, sabs=np.zeros(H))
+    r = attend_rows(qf, rows, scale, d_latent)
+    return dict(out_lat=r["out_lat"], lse=r["lse"], pc=r["p"] @ np.abs(rows[:, :d_latent]),
+                sabs=(scale * (np.abs(qf) @ np.abs(rows).T)).max(axis=1))
+
+
+def attn_weight_sums(qf, rows, lse, scale):
+    """sum_h exp(scale * qf_h . row_t - lse_h) of every token t of rows [L, d_c + d_R]: the attention
+    weight that one query row [H, d_c + d_R], of log-sum-exps lse [H], gives it over all heads; and
+    sabs = the largest scale * sum_j |q_j row_tj| [H], for an error bound."""
+    qf, rows = np.asarray(qf, np.float64), np.asarray(rows, np.float64)
+    s = scale * (qf @ rows.T)
+    w = np.exp(s - np.asarray(lse, np.float64)[:, None]).sum(axis=0)
+    return w, (scale * (np.abs(qf) @ np.abs(rows).T)).max(axis=1, initial=0.0)
+
+
+def evict_keep(weights, L: int, keep: int, sinks: int, recent: int) -> np.ndarray:
+    """Tokens (ascending) that a sequence of L tokens keeps: all when L <= keep; else the first
+    `sinks`, the last `recent`, and the keep - sinks - recent of the others with the largest weights,
+    equal weights (0 and -0 among them) by the lower token, a NaN weight below every number."""
+    if L <= keep:
+        return np.arange(L)
+    w = np.asarray(weights, np.float64)
+    middle = list(range(sinks, L - recent))
+    middle.sort(key=lambda t: (1, 0.0, t) if np.isnan(w[t]) else (0, -w[t], t))
+    chosen = middle[:keep - sinks - recent]
+    return np.array(sorted(list(range(sinks)) + chosen + list(range(L - recent, L))), dtype=np.int64)

@@ -1,0 +1,167 @@
+"""Attention with a sliding window and sinks (mla_decode_attn_window, _fp8, mla_prefill_attn_window)
+against its definition in 64 bits: a row of cached length L attends to t < sinks and t >= L - window."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from bounded_common import SCALE, RowCache, assert_window_row, f64, random_q, random_rows
+
+pytestmark = pytest.mark.gpu
+
+LENS = [0, 1, 63, 64, 65, 128, 129, 330, 700, 1000]
+MASKS = [(1, 0), (64, 0), (100, 4), (129, 64), (200, 65), (5, 128), (0, 4), (0, 0), (1 << 30, 3), (64, 1 << 30),
+         (333, 300)]
+
+
+@pytest.fixture(scope="module")
+def m():
+    assert torch.cuda.is_available()
+    import mla_latent_kv_20_b200 as lib
+    return lib
+
+
+def call(m, cache, q, window, sinks, splits=0, q_seq=None, q_len=None, stream=None, workspace=None):
+    n = q.shape[0]
+    out = torch.full((n, 128, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n, 128), 7.0, dtype=torch.float32, device="cuda")
+    nbytes = m.decode_workspace_size(n, m.window_span(cache.capacity, window, sinks), splits)
+    ws = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device="cuda") if workspace is None else workspace
+    kw = dict(window=window, sinks=sinks, lse=lse, block_table=cache.table, num_splits=splits, stream=stream)
+    if q_seq is not None:
+        m.prefill_attn_window(q, cache.data, q_seq, q_len, cache.desc, ws, out, **kw)
+    elif cache.scales is not None:
+        m.decode_attn_window_fp8(q, cache.data, cache.scales, cache.seq_lens, cache.desc, ws, out, **kw)
+    else:
+        m.decode_attn_window(q, cache.data, cache.seq_lens, cache.desc, ws, out, **kw)
+    return out, lse
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", MASKS)
+def test_decode_matches_the_definition(m, window, sinks, fp8, paged):
+    rng = np.random.default_rng(11)
+    cache = RowCache(m, [random_rows(rng, L) for L in LENS], paged, 12, fp8=fp8)
+    q = random_q(rng, len(LENS))
+    out, lse = call(m, cache, q.cuda(), window, sinks)
+    assert m.get_device_error() == 0
+    out, lse = f64(out), f64(lse)
+    for b in range(len(LENS)):
+        assert_window_row(out[b], lse[b], oracle.window_rows(f64(q[b]), cache.values[b], window, sinks, SCALE, 512))
+
+
+@pytest.mark.parametrize("splits", [1, 3, 17, 200])
+@pytest.mark.parametrize("paged", [False, True])
+def test_decode_over_forced_ranges(m, paged, splits):
+    rng = np.random.default_rng(21)
+    lens = [5000, 77, 2600, 0, 300]
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], paged, 22)
+    q = random_q(rng, len(lens))
+    out, lse = (f64(x) for x in call(m, cache, q.cuda(), 1500, 70, splits))
+    assert m.get_device_error() == 0
+    for b in range(len(lens)):
+        assert_window_row(out[b], lse[b], oracle.window_rows(f64(q[b]), cache.values[b], 1500, 70, SCALE, 512))
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("window,sinks", [(100, 4), (1, 0), (64, 65), (0, 5), (1 << 30, 0)])
+def test_rows_of_a_chunk(m, window, sinks, paged):
+    """Rows of several sequences mixed, lengths from 0, the same sequence and the same row twice."""
+    rng = np.random.default_rng(31)
+    lens = [400, 90, 650]
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], paged, 32)
+    q_seq = np.array([2, 0, 1, 0, 2, 2, 1, 0, 2, 2], np.int32)
+    q_len = np.array([650, 400, 1, 399, 0, 130, 90, 64, 650, 300], np.int32)
+    q = random_q(rng, len(q_seq))
+    q[8] = q[0]
+    out, lse = call(m, cache, q.cuda(), window, sinks, 0, torch.from_numpy(q_seq).cuda(), torch.from_numpy(q_len).cuda())
+    assert m.get_device_error() == 0
+    out, lse = f64(out), f64(lse)
+    for i, (s, L) in enumerate(zip(q_seq, q_len)):
+        assert_window_row(out[i], lse[i], oracle.window_rows(f64(q[i]), cache.values[s][:L], window, sinks, SCALE, 512))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(100, 4), (65, 0), (300, 130)])
+def test_hidden_tokens_may_hold_anything(m, window, sinks, fp8):
+    """NaN and infinities in every hidden token leave the bits of the outputs as they were."""
+    rng = np.random.default_rng(41)
+    lens = [700, 333, 200, 90]
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 42, fp8=fp8)
+    q = random_q(rng, len(lens)).cuda()
+    a = call(m, cache, q, window, sinks)
+    for b, L in enumerate(lens):
+        hidden = np.flatnonzero(~oracle.window_visible(L, window, sinks))
+        if len(hidden):
+            rows = cache.rows_of(b, hidden).cuda()
+            if fp8:
+                cache.data[rows] = 0x7F
+                cache.scales[rows] = 255
+            else:
+                cache.data[rows] = torch.tensor([float("inf"), float("-inf"), float("nan")] * 192,
+                                                dtype=torch.bfloat16, device="cuda")
+    b2 = call(m, cache, q, window, sinks)
+    assert torch.equal(a[0].view(torch.int16), b2[0].view(torch.int16)) and torch.equal(a[1], b2[1])
+    assert torch.isfinite(a[0].float()).all()
+
+
+def test_paged_and_contiguous_give_the_same_bits(m):
+    rng = np.random.default_rng(51)
+    seqs = [random_rows(rng, L) for L in (64 * 20, 1000, 130, 640)]
+    q = random_q(rng, len(seqs)).cuda()
+    a, b = (call(m, RowCache(m, seqs, paged, 52), q, 200, 68, 5) for paged in (False, True))
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+def test_a_window_over_everything_gives_the_bits_of_the_plain_decode(m):
+    rng = np.random.default_rng(61)
+    cache = RowCache(m, [random_rows(rng, L) for L in (700, 64, 1, 333)], True, 62)
+    q = random_q(rng, 4).cuda()
+    a = call(m, cache, q, 4096, 0, 6)
+    out, lse = torch.empty_like(a[0]), torch.empty_like(a[1])
+    ws = torch.empty((m.decode_workspace_size(4, cache.capacity, 6),), dtype=torch.uint8, device="cuda")
+    m.decode_attn(q, cache.data, cache.seq_lens, cache.desc, ws, out, lse=lse, block_table=cache.table, num_splits=6)
+    assert torch.equal(a[0].view(torch.int16), out.view(torch.int16)) and torch.equal(a[1], lse)
+
+
+def test_capture_and_replay_with_other_lengths(m):
+    """Captured on a side stream, replayed after the lengths and rows have changed on the device."""
+    rng = np.random.default_rng(71)
+    lens = [600, 250]
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 72)
+    q = random_q(rng, 2)
+    qd = q.cuda()
+    call(m, cache, qd, 128, 4)   # loads the kernel before the capture
+    ws = torch.empty((m.decode_workspace_size(2, cache.capacity, 0),), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        out, lse = call(m, cache, qd, 128, 4, workspace=ws)
+    for new in ([600, 250], [150, 9], [0, 250]):
+        cache.seq_lens.copy_(torch.tensor(new, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        for b in range(2):
+            ref = oracle.window_rows(f64(q[b]), cache.values[b][:new[b]], 128, 4, SCALE, 512)
+            assert_window_row(f64(out)[b], f64(lse)[b], ref)
+    assert m.get_device_error() == 0
+
+
+def test_bad_pages_and_lengths_are_reported(m):
+    rng = np.random.default_rng(81)
+    cache = RowCache(m, [random_rows(rng, 700), random_rows(rng, 700)], True, 82)
+    q = random_q(rng, 2)
+    table = cache.table.clone()
+    table[0, 5] = 1 << 29          # hidden by the window: never looked up
+    table[0, 3] = -1
+    cache.table = table
+    out, lse = call(m, cache, q.cuda(), 64, 64)
+    assert m.get_device_error() == 0
+    cache.table[0, 10] = 1 << 29   # in the window
+    call(m, cache, q.cuda(), 64, 64)
+    assert m.get_device_error() & m.DEVERR_BLOCK_RANGE
+    cache.seq_lens[1] = 10 ** 6    # clamped to the capacity
+    call(m, cache, q.cuda(), 0, 64)
+    assert m.get_device_error() & m.DEVERR_SEQLEN_RANGE
