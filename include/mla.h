@@ -124,6 +124,24 @@ mla_status mla_cache_append_fp8(const mla_bf16* c_new, const mla_bf16* kr_new, c
                                 mla_cache_desc desc, int32_t n_tokens, float rope_base, void* stream);
 
 /*
+ * (1-at) Cache append at a slot other than the position: the calls (1) and (1-fp8) with the row of
+ * token i written to slot slots[i] of its sequence, its key still rotated at pos[i].  For a cache that
+ * mla_cache_evict has shortened: the next token's slot is the sequence's length in the cache, its
+ * position the number of tokens before it.
+ *   pos [n_tokens] int32, >= 0      slots [n_tokens] int32, in [0, capacity)
+ * slots == NULL is MLA_ERR_INVALID_ARG (unless n_tokens == 0); a position or slot outside its range
+ * skips the row and sets MLA_DEVERR_POS_RANGE.
+ */
+mla_status mla_cache_append_at(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
+                               const int32_t* pos, const int32_t* slots, mla_bf16* cache,
+                               const int32_t* block_table, mla_cache_desc desc, int32_t n_tokens, float rope_base,
+                               void* stream);
+mla_status mla_cache_append_at_fp8(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
+                                   const int32_t* pos, const int32_t* slots, uint8_t* cache, uint8_t* scales,
+                                   const int32_t* block_table, mla_cache_desc desc, int32_t n_tokens,
+                                   float rope_base, void* stream);
+
+/*
  * (1') Down-projection + cache append — [DR] §2.2 (c^KV = W_D^KV h_t), §3.1 (k^R, the shared
  *      64-wide key of the RoPE branch, is projected from h_t too; c^KV and k^R are the only cached
  *      objects), §2.4 (RoPE on that branch only), §3.3 (model width d = 5120).
@@ -271,6 +289,43 @@ mla_status mla_prefill_attn_window(const mla_bf16* q_full, const mla_bf16* cache
 /* The most cached tokens (whole 64-token boxes) such a row reads when its sequence holds up to
  * max_seq_len; 0 for a negative argument. */
 int32_t mla_window_span(int32_t max_seq_len, int32_t window, int32_t sinks);
+
+/*
+ * (8) Eviction from the cache by accumulated attention weight (the pages have no counterpart).
+ * Sequence b holds L = seq_lens[b] tokens of weights weights[b * capacity + t].  If L <= keep it keeps
+ * them all.  Otherwise it keeps its first `sinks`, its last `recent` and, of those between, the
+ * keep - sinks - recent with the largest weights; equal weights (0 and -0 among them) go to the lower
+ * token, a NaN weight counts below every number.  With n = min(L, keep) and t_0 < ... < t_{n-1} the
+ * kept tokens, it writes
+ *   slot j of sequence b in cache_out = the row of t_j in cache (bit for bit; FP8: its scale byte too)
+ *   kept[b * keep + j]                = t_j for j < n, -1 for n <= j < keep
+ *   weights_out[b * capacity_out + j] = the weight of t_j for j < n, 0 for n <= j < min(L, capacity_out)
+ *   lens_out[b]                       = n
+ * and nothing else: rows and weights behind these are left as they were.
+ *   keep >= 1, sinks >= 0, recent >= 0, sinks + recent <= keep <= capacity_out, batch <= num_seqs of both
+ *   descriptors (MLA_ERR_INVALID_ARG otherwise), batch <= 16384 (MLA_ERR_UNSUPPORTED)
+ *   seq_lens [batch] int32   weights [batch, capacity] fp32   kept [batch, keep] int32
+ *   lens_out [batch] int32   weights_out [batch, capacity_out] fp32
+ *   workspace >= mla_evict_workspace_size(batch, keep) bytes, 16-byte aligned
+ * In place: cache_out == cache (FP8: scales_out == scales too), page size and, contiguous, max_seq_len
+ * of the two descriptors equal; slots of cache_out must then be the same sequence's own slots at the
+ * same place, or pages that no sequence's tokens are read from.  Otherwise the two buffers must not meet
+ * (MLA_ERR_INVALID_ARG).  weights_out may be weights where the capacities are equal, lens_out may be
+ * seq_lens; no other outputs may overlap inputs.  A length outside [0, capacity] is clamped
+ * (MLA_DEVERR_SEQLEN_RANGE); a row whose block id is out of range is skipped (MLA_DEVERR_BLOCK_RANGE).
+ */
+size_t mla_evict_workspace_size(int32_t batch, int32_t keep);
+mla_status mla_cache_evict(const mla_bf16* cache, const int32_t* block_table, const int32_t* seq_lens,
+                           const float* weights, mla_cache_desc desc, int32_t batch, int32_t keep, int32_t sinks,
+                           int32_t recent, mla_bf16* cache_out, const int32_t* block_table_out,
+                           mla_cache_desc desc_out, int32_t* kept, int32_t* lens_out, float* weights_out,
+                           void* workspace, size_t workspace_bytes, void* stream);
+mla_status mla_cache_evict_fp8(const uint8_t* cache, const uint8_t* scales, const int32_t* block_table,
+                               const int32_t* seq_lens, const float* weights, mla_cache_desc desc, int32_t batch,
+                               int32_t keep, int32_t sinks, int32_t recent, uint8_t* cache_out, uint8_t* scales_out,
+                               const int32_t* block_table_out, mla_cache_desc desc_out, int32_t* kept,
+                               int32_t* lens_out, float* weights_out, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /*
  * (3-fp8) Decode attention over an FP8 latent cache — [DR] §4.2 效率证据 (FP8 KV cache) with the

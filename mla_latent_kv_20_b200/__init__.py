@@ -68,6 +68,13 @@ def _load():
         "mla_prefill_attn_window": (ctypes.c_int,
                                     [P, P, P, P, P, CacheDesc, I32, I32, I32, F32, I32, P, SZ, P, P, P]),
         "mla_window_span": (I32, [I32, I32, I32]),
+        "mla_cache_append_at": (ctypes.c_int, [P, P, P, P, P, P, P, CacheDesc, I32, F32, P]),
+        "mla_cache_append_at_fp8": (ctypes.c_int, [P, P, P, P, P, P, P, P, CacheDesc, I32, F32, P]),
+        "mla_evict_workspace_size": (SZ, [I32, I32]),
+        "mla_cache_evict": (ctypes.c_int, [P, P, P, P, CacheDesc, I32, I32, I32, I32, P, P, CacheDesc, P, P, P, P, SZ,
+                                           P]),
+        "mla_cache_evict_fp8": (ctypes.c_int, [P, P, P, P, P, CacheDesc, I32, I32, I32, I32, P, P, P, CacheDesc, P, P,
+                                               P, P, SZ, P]),
         "mla_unabsorb_v": (ctypes.c_int, [P, P, P, I32, P]),
         "mla_decode_attn_noalloc": (ctypes.c_int, [P, P, P, P, CacheDesc, I32, F32, I32, P, P, P]),
         "mla_noalloc_scratch_bytes": (SZ, []),
@@ -123,6 +130,24 @@ def cache_append_fp8(c_new, kr_new, pos, cache, scales, desc: CacheDesc, *, seq_
     n = c_new.shape[0] if n_tokens is None else n_tokens
     _check(lib.mla_cache_append_fp8(_ptr(c_new), _ptr(kr_new), _ptr(seq_ids), _ptr(pos), _ptr(cache), _ptr(scales),
                                     _ptr(block_table), desc, n, rope_base, _stream(stream)), "mla_cache_append_fp8")
+
+
+def cache_append_at(c_new, kr_new, pos, slots, cache, desc: CacheDesc, *, seq_ids=None, block_table=None,
+                    rope_base: float = 10000.0, stream=None, n_tokens: int | None = None):
+    """mla_cache_append_at: token i's row goes to slot slots[i], its key is rotated at pos[i] (a cache
+    shortened by cache_evict)."""
+    n = c_new.shape[0] if n_tokens is None else n_tokens
+    _check(lib.mla_cache_append_at(_ptr(c_new), _ptr(kr_new), _ptr(seq_ids), _ptr(pos), _ptr(slots), _ptr(cache),
+                                   _ptr(block_table), desc, n, rope_base, _stream(stream)), "mla_cache_append_at")
+
+
+def cache_append_at_fp8(c_new, kr_new, pos, slots, cache, scales, desc: CacheDesc, *, seq_ids=None, block_table=None,
+                        rope_base: float = 10000.0, stream=None, n_tokens: int | None = None):
+    """mla_cache_append_at_fp8: cache_append_at into an FP8 cache."""
+    n = c_new.shape[0] if n_tokens is None else n_tokens
+    _check(lib.mla_cache_append_at_fp8(_ptr(c_new), _ptr(kr_new), _ptr(seq_ids), _ptr(pos), _ptr(slots), _ptr(cache),
+                                       _ptr(scales), _ptr(block_table), desc, n, rope_base, _stream(stream)),
+           "mla_cache_append_at_fp8")
 
 
 def project_append(h, w_dkv, w_kr, pos, cache, desc: CacheDesc, *, seq_ids=None, block_table=None,
@@ -238,6 +263,39 @@ def prefill_attn_window(q_full, cache, q_seq, q_len, desc: CacheDesc, workspace,
     _check(lib.mla_prefill_attn_window(_ptr(q_full), _ptr(cache), _ptr(block_table), _ptr(q_seq), _ptr(q_len), desc, n,
                                        window, sinks, softmax_scale, num_splits, _ptr(workspace), wb, _ptr(out_lat),
                                        _ptr(lse), _stream(stream)), "mla_prefill_attn_window")
+
+
+def evict_workspace_size(batch: int, keep: int) -> int:
+    return lib.mla_evict_workspace_size(batch, keep)
+
+
+def cache_evict(cache, seq_lens, weights, desc: CacheDesc, kept, lens_out, weights_out, workspace, *, keep: int,
+                sinks: int = 0, recent: int = 0, block_table=None, cache_out=None, desc_out: CacheDesc | None = None,
+                block_table_out=None, stream=None, batch: int | None = None, workspace_bytes: int | None = None):
+    """mla_cache_evict: each sequence longer than `keep` keeps its first `sinks`, its last `recent` and the
+    heaviest tokens between, moved in order to the front of cache_out, or (cache_out None) of the same cache."""
+    b = seq_lens.shape[0] if batch is None else batch
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    if cache_out is None:
+        cache_out, desc_out, block_table_out = cache, desc, block_table
+    _check(lib.mla_cache_evict(_ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(weights), desc, b, keep, sinks,
+                               recent, _ptr(cache_out), _ptr(block_table_out), desc_out, _ptr(kept), _ptr(lens_out),
+                               _ptr(weights_out), _ptr(workspace), wb, _stream(stream)), "mla_cache_evict")
+
+
+def cache_evict_fp8(cache, scales, seq_lens, weights, desc: CacheDesc, kept, lens_out, weights_out, workspace, *,
+                    keep: int, sinks: int = 0, recent: int = 0, block_table=None, cache_out=None, scales_out=None,
+                    desc_out: CacheDesc | None = None, block_table_out=None, stream=None, batch: int | None = None,
+                    workspace_bytes: int | None = None):
+    """mla_cache_evict_fp8: cache_evict over an FP8 cache (codes and row scales)."""
+    b = seq_lens.shape[0] if batch is None else batch
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    if cache_out is None:
+        cache_out, scales_out, desc_out, block_table_out = cache, scales, desc, block_table
+    _check(lib.mla_cache_evict_fp8(_ptr(cache), _ptr(scales), _ptr(block_table), _ptr(seq_lens), _ptr(weights), desc, b,
+                                   keep, sinks, recent, _ptr(cache_out), _ptr(scales_out), _ptr(block_table_out),
+                                   desc_out, _ptr(kept), _ptr(lens_out), _ptr(weights_out), _ptr(workspace), wb,
+                                   _stream(stream)), "mla_cache_evict_fp8")
 
 
 NOALLOC_SCRATCH_BYTES = int(lib.mla_noalloc_scratch_bytes())   # the library's own constant

@@ -65,22 +65,25 @@ __device__ __forceinline__ __nv_bfloat162 rope_pair(__nv_bfloat162 x, double c, 
 
 // One CTA of 96 threads per new token: threads 0..63 copy the latent (16 B each), threads
 // 64..95 rotate one pair of the 64-wide key each (one fp64 sincos per thread, all in parallel).
+// The row goes to slot pos[i] of its sequence, or to slots[i] where those are given.
 __global__ void __launch_bounds__(96) cache_append_kernel(const uint4* __restrict__ c_new,
                                                           const __nv_bfloat162* __restrict__ kr_new,
                                                           const int32_t* __restrict__ seq_ids,
-                                                          const int32_t* __restrict__ pos, uint4* cache,
+                                                          const int32_t* __restrict__ pos,
+                                                          const int32_t* __restrict__ slots, uint4* cache,
                                                           CacheView v, RopeFreq f) {
   pdl_trigger();
   pdl_wait();
   const int i = blockIdx.x;
   const int seq = seq_ids ? seq_ids[i] : i;
   const int p = pos[i];
+  const int slot = slots ? slots[i] : p;
   const int capacity = v.page_size == 0 ? v.max_seq_len : v.max_blocks * kPage;
-  if (p < 0 || p >= capacity || seq < 0 || seq >= v.num_seqs) {
+  if (p < 0 || slot < 0 || slot >= capacity || seq < 0 || seq >= v.num_seqs) {
     if (threadIdx.x == 0) set_dev_error(0x1);
     return;
   }
-  const int64_t row = cache_row(v, seq, p);
+  const int64_t row = cache_row(v, seq, slot);
   if (row < 0) return;
   const int t = threadIdx.x;
   if (t < 64) {
@@ -132,7 +135,8 @@ __device__ __forceinline__ int fp8_scale_exp(double amax) {
 __global__ void __launch_bounds__(96) cache_append_fp8_kernel(const uint4* __restrict__ c_new,
                                                               const __nv_bfloat162* __restrict__ kr_new,
                                                               const int32_t* __restrict__ seq_ids,
-                                                              const int32_t* __restrict__ pos, uint8_t* cache,
+                                                              const int32_t* __restrict__ pos,
+                                                              const int32_t* __restrict__ slots, uint8_t* cache,
                                                               uint8_t* scales, CacheView v, RopeFreq f) {
   __shared__ double red[3];
   pdl_trigger();
@@ -140,12 +144,13 @@ __global__ void __launch_bounds__(96) cache_append_fp8_kernel(const uint4* __res
   const int i = blockIdx.x;
   const int seq = seq_ids ? seq_ids[i] : i;
   const int p = pos[i];
+  const int slot = slots ? slots[i] : p;
   const int capacity = v.page_size == 0 ? v.max_seq_len : v.max_blocks * kPage;
-  if (p < 0 || p >= capacity || seq < 0 || seq >= v.num_seqs) {   // the same for every thread of the CTA
+  if (p < 0 || slot < 0 || slot >= capacity || seq < 0 || seq >= v.num_seqs) {   // the same for every thread of the CTA
     if (threadIdx.x == 0) set_dev_error(0x1);
     return;
   }
-  const int64_t row = cache_row(v, seq, p);
+  const int64_t row = cache_row(v, seq, slot);
   if (row < 0) return;
   const int t = threadIdx.x;
   double x[8];

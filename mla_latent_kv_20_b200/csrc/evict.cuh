@@ -1,0 +1,340 @@
+// evict.cuh — eviction from the latent cache by accumulated attention weight.
+//
+// A sequence of L > keep tokens keeps its first `sinks`, its last `recent`, and of those between
+// them the k = keep - sinks - recent with the largest weights (equal weights by the lower token, NaN
+// below every number); L <= keep keeps all.  The kept tokens' rows move, in order, to slots
+// 0 .. n - 1 of the same cache or of another one.
+//
+// Two kernels.  The selection finds the k-th largest weight by its bits (a radix select: four 8-bit
+// digits from the top, each one histogram of the keys that share the digits found so far), then
+// numbers the kept tokens in order.  A cluster of CTAs shares a sequence: each holds the order keys
+// of its slice in shared memory, and the histograms are summed through distributed shared memory.
+// The move is a copy bound by HBM: the rows' bytes read once and written once.
+#pragma once
+
+#include "append.cuh"
+#include "decode_common.cuh"
+
+namespace mla {
+
+constexpr int kEvThreads = 1024;
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvKeys = 16384;        // order keys a CTA holds in shared memory (a longer slice is read again)
+constexpr int kEvMaxCluster = 8;
+
+// Workspace: the kept tokens' weights [batch][keep] fp32 and the lengths before the eviction [batch].
+// The move kernel reads these alone, so weights_out may be weights, and lens_out seq_lens.
+struct EvictWorkspace {
+  float* w;
+  int32_t* len;
+};
+__host__ __device__ __forceinline__ EvictWorkspace ev_carve(void* base, int batch, int keep) {
+  EvictWorkspace e;
+  e.w = reinterpret_cast<float*>(base);
+  e.len = reinterpret_cast<int32_t*>(e.w + static_cast<int64_t>(batch) * keep);
+  return e;
+}
+__host__ __device__ __forceinline__ size_t ev_ws_bytes(int batch, int keep) {
+  return ((static_cast<size_t>(batch) * keep + batch) * 4 + 15) / 16 * 16;
+}
+
+struct EvSmem {
+  uint32_t keys[kEvKeys];
+  uint32_t hist[256 * 32];        // [digit][lane]: the lanes of a warp never meet in a bank or a counter
+  uint32_t total[2][256];         // this CTA's histogram, read by the cluster (two passes alternate)
+  uint32_t sums[256];             // the cluster's
+  uint32_t count[2];              // this CTA's keys above and at the threshold, read by the cluster
+  uint32_t warp_gt[kEvWarps], warp_eq[kEvWarps];
+  uint32_t digit, above;
+};
+
+// Weights in order as unsigned numbers: -inf < ... < -0 = 0 < ... < inf, and NaN (0) below them all.
+__device__ __forceinline__ uint32_t ev_key(float w) {
+  const uint32_t u = __float_as_uint(w);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
+  if ((u << 1) == 0u) return 0x80000000u;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+// grid = batch * C CTAs in clusters of C: cluster b selects for sequence b.
+__global__ void __launch_bounds__(kEvThreads, 1)
+    evict_select_kernel(const float* __restrict__ weights, const int32_t* __restrict__ seq_lens, int capacity, int keep,
+                        int sinks, int recent, int C, int32_t* __restrict__ kept, EvictWorkspace ws) {
+  extern __shared__ __align__(16) uint8_t ev_raw[];
+  EvSmem& sm = *reinterpret_cast<EvSmem*>(ev_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / C;
+  const int rank = blockIdx.x - b * C;
+  pdl_trigger();
+  pdl_wait();
+  int L = seq_lens[b];
+  if (L < 0 || L > capacity) {
+    if (tid == 0 && rank == 0) set_dev_error(0x4);
+    L = L < 0 ? 0 : capacity;
+  }
+  if (tid == 0 && rank == 0) ws.len[b] = L;
+  const float* w = weights + static_cast<int64_t>(b) * capacity;
+  int32_t* kp = kept + static_cast<int64_t>(b) * keep;
+  float* kw = ws.w + static_cast<int64_t>(b) * keep;
+  const int me = rank * kEvThreads + tid, all = C * kEvThreads;
+  if (L <= keep) {   // the same in every CTA of the cluster: none of them reaches a cluster barrier
+    for (int j = me; j < keep; j += all) {
+      kp[j] = j < L ? j : -1;
+      kw[j] = j < L ? w[j] : 0.f;
+    }
+    return;
+  }
+  for (int j = me; j < sinks; j += all) {
+    kp[j] = j;
+    kw[j] = w[j];
+  }
+  for (int j = me; j < recent; j += all) {
+    kp[keep - recent + j] = L - recent + j;
+    kw[keep - recent + j] = w[L - recent + j];
+  }
+  const int k = keep - sinks - recent;
+  if (k == 0) return;
+  // This CTA's slice of the middle, in order: tokens first + [0, n).
+  const int M = L - sinks - recent;   // > k
+  const int S = (M + C - 1) / C;
+  const int first = sinks + min(M, rank * S);
+  const int n = min(M - min(M, rank * S), S);
+  for (int i = tid; i < min(n, kEvKeys); i += kEvThreads) sm.keys[i] = ev_key(w[first + i]);
+  auto key_at = [&](int i) { return i < kEvKeys ? sm.keys[i] : ev_key(w[first + i]); };
+
+  uint32_t prefix = 0, k_rem = static_cast<uint32_t>(k);
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = tid; i < 256 * 32; i += kEvThreads) sm.hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kEvThreads) {
+      const uint32_t key = key_at(i);
+      if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&sm.hist[((key >> shift) & 255u) * 32 + lane], 1u);
+    }
+    __syncthreads();
+    {   // digit d summed by four threads, eight counters each, every one from a bank of its own
+      const int d = tid >> 2, q = tid & 3;
+      uint32_t s = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += sm.hist[d * 32 + ((8 * q + u + d) & 31)];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (q == 0) sm.total[pass & 1][d] = s;
+    }
+    cluster_sync();
+    if (tid < 256) {
+      uint32_t s = 0;
+      for (int c = 0; c < C; ++c) s += ld_dsmem_u32(&sm.total[pass & 1][tid], c);
+      sm.sums[tid] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {   // the digit of the k-th largest: lane l takes digits 255 - 8 l .. 248 - 8 l
+      uint32_t c8[8], s = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        c8[u] = sm.sums[255 - 8 * lane - u];
+        s += c8[u];
+      }
+      uint32_t incl = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      uint32_t above = incl - s;
+      if (above < k_rem && incl >= k_rem) {
+        int u = 0;
+        while (above + c8[u] < k_rem) above += c8[u++];
+        sm.digit = 255u - 8u * lane - u;
+        sm.above = above;
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | sm.digit;
+    k_rem -= sm.above;
+  }
+  const uint32_t thr = prefix;   // keys above it are kept, and the first k_rem of those equal to it
+
+  // Number the kept tokens: warp w walks its part of the slice in order, 32 at a time.
+  const int per = ((n + kEvWarps - 1) / kEvWarps + 31) & ~31;
+  const int lo = min(n, warp * per), hi = min(n, lo + per);
+  uint32_t gt = 0, eq = 0;
+  for (int i = lo; i < hi; i += 32) {
+    const bool in = i + lane < hi;
+    const uint32_t key = in ? key_at(i + lane) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, in && key > thr));
+    eq += __popc(__ballot_sync(0xffffffffu, in && key == thr));
+  }
+  if (lane == 0) {
+    sm.warp_gt[warp] = gt;
+    sm.warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t g = sm.warp_gt[lane], e = sm.warp_eq[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, g, o), y = __shfl_up_sync(0xffffffffu, e, o);
+      if (lane >= o) {
+        g += x;
+        e += y;
+      }
+    }
+    if (lane == 31) {
+      sm.count[0] = g;
+      sm.count[1] = e;
+    }
+    sm.warp_gt[lane] = g - sm.warp_gt[lane];   // before this warp, within the slice
+    sm.warp_eq[lane] = e - sm.warp_eq[lane];
+  }
+  cluster_sync();
+  uint32_t g0 = sm.warp_gt[warp], e0 = sm.warp_eq[warp];
+  for (int c = 0; c < rank; ++c) {
+    g0 += ld_dsmem_u32(&sm.count[0], c);
+    e0 += ld_dsmem_u32(&sm.count[1], c);
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = lo; i < hi; i += 32) {
+    const bool in = i + lane < hi;
+    const uint32_t key = in ? key_at(i + lane) : 0u;
+    const uint32_t bg = __ballot_sync(0xffffffffu, in && key > thr);
+    const uint32_t be = __ballot_sync(0xffffffffu, in && key == thr);
+    const uint32_t e = e0 + __popc(be & below);
+    if (in && (key > thr || (key == thr && e < k_rem))) {
+      const int j = sinks + static_cast<int>(g0 + __popc(bg & below) + min(e, k_rem));
+      const int t = first + i + lane;
+      kp[j] = t;
+      kw[j] = w[t];
+    }
+    g0 += __popc(bg);
+    e0 += __popc(be);
+  }
+  cluster_sync();   // no CTA leaves while another reads its counts
+}
+
+// A cache of rows of `row_bytes` bytes (1152 bf16, 576 FP8) with, for FP8, a scale byte per row.
+struct EvictCache {
+  CacheView v;
+  uint8_t* rows;
+  uint8_t* scales;
+};
+
+// What the move writes beside the rows: the weights at their new slots, zeros in the slots that the
+// eviction freed (up to the old length), and the new lengths.
+__device__ __forceinline__ void ev_write_weights(const EvictWorkspace& ws, int b, int L, int keep, int capacity_out,
+                                                 float* weights_out, int32_t* lens_out) {
+  const int n = min(L, keep);
+  float* wo = weights_out + static_cast<int64_t>(b) * capacity_out;
+  const float* kw = ws.w + static_cast<int64_t>(b) * keep;
+  for (int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; j < min(L, capacity_out);
+       j += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    wo[j] = j < n ? kw[j] : 0.f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) lens_out[b] = n;
+}
+
+// Move into another buffer: grid = (blocks of kEvRows slots, batch).  Every row on its own, so the
+// loads of a thread (nine 16-byte pieces for bf16) are all in flight together.
+constexpr int kEvRows = 32;
+template <int kRowBytes>
+__global__ void __launch_bounds__(256) evict_copy_kernel(EvictCache src, EvictCache dst, const int32_t* __restrict__ kept,
+                                                         EvictWorkspace ws, int keep, int capacity_out,
+                                                         float* weights_out, int32_t* lens_out) {
+  constexpr int kPieces = kRowBytes / 16;
+  constexpr int kPer = (kEvRows * kPieces + 255) / 256;
+  __shared__ int64_t from[kEvRows], to[kEvRows];
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y;
+  const int L = ws.len[b];
+  const int n = min(L, keep);
+  const int j0 = blockIdx.x * kEvRows;
+  if (threadIdx.x < kEvRows) {
+    const int j = j0 + threadIdx.x;
+    int64_t s = -1, d = -1;
+    if (j < n) {
+      s = cache_row(src.v, b, kept[static_cast<int64_t>(b) * keep + j]);
+      d = cache_row(dst.v, b, j);
+      if (s < 0 || d < 0) s = d = -1;
+      if (s >= 0 && src.scales != nullptr) dst.scales[d] = src.scales[s];
+    }
+    from[threadIdx.x] = s;
+    to[threadIdx.x] = d;
+  }
+  __syncthreads();
+  uint4 x[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = u * 256 + threadIdx.x;
+    const int r = i / kPieces;
+    if (r < kEvRows && from[r] >= 0) x[u] = reinterpret_cast<const uint4*>(src.rows + from[r] * kRowBytes)[i - r * kPieces];
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = u * 256 + threadIdx.x;
+    const int r = i / kPieces;
+    if (r < kEvRows && from[r] >= 0) reinterpret_cast<uint4*>(dst.rows + to[r] * kRowBytes)[i - r * kPieces] = x[u];
+  }
+  ev_write_weights(ws, b, L, keep, capacity_out, weights_out, lens_out);
+}
+
+// Move within one buffer: grid = (9 column slices, batch).  A kept token never moves to a later slot,
+// so a slice of the columns can be moved in order of the slots by one CTA: it reads the pieces of 256
+// slots, waits until all its threads have, and writes them; whatever a write overwrites belongs to a
+// token that was evicted or has been read.  The slices do not meet, so no CTA waits for another.
+template <int kRowBytes>
+__global__ void __launch_bounds__(256) evict_compact_kernel(EvictCache src, EvictCache dst,
+                                                            const int32_t* __restrict__ kept, EvictWorkspace ws,
+                                                            int keep, int capacity_out, float* weights_out,
+                                                            int32_t* lens_out) {
+  constexpr int kSlices = 9;
+  constexpr int kPieces = kRowBytes / 16 / kSlices;   // 16-byte pieces of a row in a slice
+  constexpr int kStep = 256;                          // slots at a time
+  __shared__ int64_t from[kStep], to[kStep];
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y;
+  const int L = ws.len[b];
+  const int n = min(L, keep);
+  const int tid = threadIdx.x;
+  const int col = blockIdx.x * kPieces + tid % kPieces;
+  for (int j0 = 0; j0 < n; j0 += kStep) {
+    {
+      const int j = j0 + tid;
+      int64_t s = -1, d = -1;
+      if (j < n) {
+        s = cache_row(src.v, b, kept[static_cast<int64_t>(b) * keep + j]);
+        d = cache_row(dst.v, b, j);
+        if (s < 0 || d < 0 || s == d) s = d = -1;
+      }
+      from[tid] = s;
+      to[tid] = d;
+    }
+    __syncthreads();
+    uint4 x[kPieces];
+    uint8_t sc = 0;
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int64_t s = from[u * (kStep / kPieces) + tid / kPieces];
+      if (s >= 0) x[u] = reinterpret_cast<const uint4*>(src.rows + s * kRowBytes)[col];
+    }
+    const bool scale = blockIdx.x == 0 && src.scales != nullptr && from[tid] >= 0;
+    if (scale) sc = src.scales[from[tid]];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int r = u * (kStep / kPieces) + tid / kPieces;
+      if (from[r] >= 0) reinterpret_cast<uint4*>(dst.rows + to[r] * kRowBytes)[col] = x[u];
+    }
+    if (scale) dst.scales[to[tid]] = sc;
+    __syncthreads();   // from and to are read above
+  }
+  ev_write_weights(ws, b, L, keep, capacity_out, weights_out, lens_out);
+}
+
+}  // namespace mla

@@ -18,6 +18,7 @@
 #include "decode_common.cuh"
 #include "decode_tc.cuh"
 #include "down_proj.cuh"
+#include "evict.cuh"
 #include "out_proj.cuh"
 #include "gemm_tc.cuh"
 #include "ptx.cuh"
@@ -184,6 +185,43 @@ mla::RopeFreq rope_freq(float rope_base) {
   return f;
 }
 
+// Append at slot pos[i], or at slots[i] where they are given.
+mla_status launch_append(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids, const int32_t* pos,
+                         const int32_t* slots, mla_bf16* cache, const int32_t* block_table, mla_cache_desc desc,
+                         int32_t n_tokens, float rope_base, void* stream) {
+  if (n_tokens < 0 || !(rope_base > 0.f) || !std::isfinite(rope_base)) return MLA_ERR_INVALID_ARG;
+  CacheView v;
+  const mla_status st = check_cache(desc, cache, block_table, &v);
+  if (st != MLA_OK) return st;
+  if (n_tokens == 0) return MLA_OK;
+  if (c_new == nullptr || kr_new == nullptr || pos == nullptr || !aligned16(c_new) || !aligned16(kr_new))
+    return MLA_ERR_INVALID_ARG;
+  if (seq_ids == nullptr && n_tokens > desc.num_seqs) return MLA_ERR_INVALID_ARG;
+  if (n_tokens > INT_MAX / 2) return MLA_ERR_UNSUPPORTED;
+  return launch_chained(mla::cache_append_kernel, dim3(n_tokens), dim3(96), 0, as_stream(stream),
+                        reinterpret_cast<const uint4*>(c_new), reinterpret_cast<const __nv_bfloat162*>(kr_new),
+                        seq_ids, pos, slots, reinterpret_cast<uint4*>(cache), v, rope_freq(rope_base));
+}
+
+mla_status launch_append_fp8(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
+                             const int32_t* pos, const int32_t* slots, uint8_t* cache, uint8_t* scales,
+                             const int32_t* block_table, mla_cache_desc desc, int32_t n_tokens, float rope_base,
+                             void* stream) {
+  if (n_tokens < 0 || !(rope_base > 0.f) || !std::isfinite(rope_base)) return MLA_ERR_INVALID_ARG;
+  CacheView v;
+  const mla_status st = check_cache(desc, cache, block_table, &v);
+  if (st != MLA_OK) return st;
+  if (n_tokens == 0) return MLA_OK;
+  if (scales == nullptr) return MLA_ERR_INVALID_ARG;
+  if (c_new == nullptr || kr_new == nullptr || pos == nullptr || !aligned16(c_new) || !aligned16(kr_new))
+    return MLA_ERR_INVALID_ARG;
+  if (seq_ids == nullptr && n_tokens > desc.num_seqs) return MLA_ERR_INVALID_ARG;
+  if (n_tokens > INT_MAX / 2) return MLA_ERR_UNSUPPORTED;
+  return launch_chained(mla::cache_append_fp8_kernel, dim3(n_tokens), dim3(96), 0, as_stream(stream),
+                        reinterpret_cast<const uint4*>(c_new), reinterpret_cast<const __nv_bfloat162*>(kr_new),
+                        seq_ids, pos, slots, cache, scales, v, rope_freq(rope_base));
+}
+
 // The output projection for one tile size NT: per N tile of NT sequences, the split kernel (one
 // CTA per SM, each an equal share of W_O) and the kernel that sums its partials.
 template <int NT, int R>
@@ -258,36 +296,30 @@ extern "C" {
 mla_status mla_cache_append(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
                             const int32_t* pos, mla_bf16* cache, const int32_t* block_table,
                             mla_cache_desc desc, int32_t n_tokens, float rope_base, void* stream) {
-  if (n_tokens < 0 || !(rope_base > 0.f) || !std::isfinite(rope_base)) return MLA_ERR_INVALID_ARG;
-  CacheView v;
-  const mla_status st = check_cache(desc, cache, block_table, &v);
-  if (st != MLA_OK) return st;
-  if (n_tokens == 0) return MLA_OK;
-  if (c_new == nullptr || kr_new == nullptr || pos == nullptr || !aligned16(c_new) || !aligned16(kr_new))
-    return MLA_ERR_INVALID_ARG;
-  if (seq_ids == nullptr && n_tokens > desc.num_seqs) return MLA_ERR_INVALID_ARG;
-  if (n_tokens > INT_MAX / 2) return MLA_ERR_UNSUPPORTED;
-  return launch_chained(mla::cache_append_kernel, dim3(n_tokens), dim3(96), 0, as_stream(stream),
-                        reinterpret_cast<const uint4*>(c_new), reinterpret_cast<const __nv_bfloat162*>(kr_new),
-                        seq_ids, pos, reinterpret_cast<uint4*>(cache), v, rope_freq(rope_base));
+  return launch_append(c_new, kr_new, seq_ids, pos, nullptr, cache, block_table, desc, n_tokens, rope_base, stream);
+}
+
+mla_status mla_cache_append_at(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
+                               const int32_t* pos, const int32_t* slots, mla_bf16* cache, const int32_t* block_table,
+                               mla_cache_desc desc, int32_t n_tokens, float rope_base, void* stream) {
+  if (n_tokens > 0 && slots == nullptr) return MLA_ERR_INVALID_ARG;
+  return launch_append(c_new, kr_new, seq_ids, pos, slots, cache, block_table, desc, n_tokens, rope_base, stream);
 }
 
 mla_status mla_cache_append_fp8(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
                                 const int32_t* pos, uint8_t* cache, uint8_t* scales, const int32_t* block_table,
                                 mla_cache_desc desc, int32_t n_tokens, float rope_base, void* stream) {
-  if (n_tokens < 0 || !(rope_base > 0.f) || !std::isfinite(rope_base)) return MLA_ERR_INVALID_ARG;
-  CacheView v;
-  const mla_status st = check_cache(desc, cache, block_table, &v);
-  if (st != MLA_OK) return st;
-  if (n_tokens == 0) return MLA_OK;
-  if (scales == nullptr) return MLA_ERR_INVALID_ARG;
-  if (c_new == nullptr || kr_new == nullptr || pos == nullptr || !aligned16(c_new) || !aligned16(kr_new))
-    return MLA_ERR_INVALID_ARG;
-  if (seq_ids == nullptr && n_tokens > desc.num_seqs) return MLA_ERR_INVALID_ARG;
-  if (n_tokens > INT_MAX / 2) return MLA_ERR_UNSUPPORTED;
-  return launch_chained(mla::cache_append_fp8_kernel, dim3(n_tokens), dim3(96), 0, as_stream(stream),
-                        reinterpret_cast<const uint4*>(c_new), reinterpret_cast<const __nv_bfloat162*>(kr_new),
-                        seq_ids, pos, cache, scales, v, rope_freq(rope_base));
+  return launch_append_fp8(c_new, kr_new, seq_ids, pos, nullptr, cache, scales, block_table, desc, n_tokens, rope_base,
+                           stream);
+}
+
+mla_status mla_cache_append_at_fp8(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
+                                   const int32_t* pos, const int32_t* slots, uint8_t* cache, uint8_t* scales,
+                                   const int32_t* block_table, mla_cache_desc desc, int32_t n_tokens, float rope_base,
+                                   void* stream) {
+  if (n_tokens > 0 && slots == nullptr) return MLA_ERR_INVALID_ARG;
+  return launch_append_fp8(c_new, kr_new, seq_ids, pos, slots, cache, scales, block_table, desc, n_tokens, rope_base,
+                           stream);
 }
 
 mla_status mla_project_append(const mla_bf16* h, const mla_bf16* w_dkv, const mla_bf16* w_kr,
@@ -512,6 +544,130 @@ mla_status mla_prefill_attn_window(const mla_bf16* q_full, const mla_bf16* cache
   const mla::WindowRows win{window, sinks};
   return launch_attn(q_full, cache, block_table, q_len, q_seq, desc, n_queries, softmax_scale, num_splits, workspace,
                      workspace_bytes, out_lat, lse, stream, nullptr, &win);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// Eviction by accumulated attention weight.
+// ------------------------------------------------------------------------------------------
+namespace {
+
+// Launch in clusters of `cluster` CTAs along x, chained like launch_chained.
+template <typename... KArgs, typename... Args>
+mla_status launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block, unsigned cluster, size_t smem,
+                           cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
+}
+
+// Whether [a, a + n) and [b, b + m) share a byte.
+bool ranges_meet(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uint64_t>(m) && y < x + static_cast<uint64_t>(n);
+}
+
+mla_status launch_evict(const void* cache, const uint8_t* scales, const int32_t* block_table, const int32_t* seq_lens,
+                        const float* weights, mla_cache_desc desc, int32_t batch, int32_t keep, int32_t sinks,
+                        int32_t recent, void* cache_out, uint8_t* scales_out, const int32_t* block_table_out,
+                        mla_cache_desc desc_out, int32_t* kept, int32_t* lens_out, float* weights_out, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const bool fp8 = scales != nullptr;
+  const int row_bytes = fp8 ? mla::kDRow : 2 * mla::kDRow;
+  if (batch < 0 || keep < 1 || sinks < 0 || recent < 0) return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(sinks) + recent > keep) return MLA_ERR_INVALID_ARG;
+  if (batch > mla::kMaxDecodeBatch) return MLA_ERR_UNSUPPORTED;
+  CacheView v, vo;
+  mla_status st = check_cache(desc, cache, block_table, &v);
+  if (st == MLA_OK) st = check_cache(desc_out, cache_out, block_table_out, &vo);
+  if (st != MLA_OK) return st;
+  const int capacity = cache_capacity(desc), capacity_out = cache_capacity(desc_out);
+  if (keep > capacity_out) return MLA_ERR_INVALID_ARG;
+  if (batch > desc.num_seqs || batch > desc_out.num_seqs) return MLA_ERR_INVALID_ARG;
+  // The same buffer in the same layout, or two that do not meet.
+  const bool in_place = cache_out == cache;
+  if (in_place) {
+    if (desc.page_size != desc_out.page_size || scales != scales_out) return MLA_ERR_INVALID_ARG;
+    if (desc.page_size == 0 && desc.max_seq_len != desc_out.max_seq_len) return MLA_ERR_INVALID_ARG;
+  } else {
+    if (ranges_meet(cache, desc.num_rows * row_bytes, cache_out, desc_out.num_rows * row_bytes))
+      return MLA_ERR_INVALID_ARG;
+    if (fp8 && ranges_meet(scales, desc.num_rows, scales_out, desc_out.num_rows)) return MLA_ERR_INVALID_ARG;
+  }
+  if (batch == 0) return MLA_OK;
+  if (seq_lens == nullptr || weights == nullptr || kept == nullptr || lens_out == nullptr || weights_out == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < mla::ev_ws_bytes(batch, keep))
+    return MLA_ERR_WORKSPACE;
+  // CTAs per sequence: one per 4096 tokens of capacity, while the clusters together fit the SMs.
+  int C = 1;
+  while (C < mla::kEvMaxCluster && capacity / C > 4096 && 2 * C * batch <= device_sm_count()) C *= 2;
+  const mla::EvictWorkspace ws = mla::ev_carve(workspace, batch, keep);
+  if (cudaFuncSetAttribute(mla::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(mla::EvSmem))) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  cudaStream_t s = as_stream(stream);
+  st = launch_clusters(mla::evict_select_kernel, dim3(batch * C), dim3(mla::kEvThreads), C, sizeof(mla::EvSmem), s,
+                       weights, seq_lens, capacity, keep, sinks, recent, C, kept, ws);
+  if (st != MLA_OK) return st;
+  const mla::EvictCache src{v, static_cast<uint8_t*>(const_cast<void*>(cache)), const_cast<uint8_t*>(scales)};
+  const mla::EvictCache dst{vo, static_cast<uint8_t*>(cache_out), scales_out};
+  if (in_place)
+    return launch_chained(fp8 ? mla::evict_compact_kernel<mla::kDRow> : mla::evict_compact_kernel<2 * mla::kDRow>,
+                          dim3(9, batch), dim3(256), 0, s, src, dst, static_cast<const int32_t*>(kept), ws, keep,
+                          capacity_out, weights_out, lens_out);
+  return launch_chained(fp8 ? mla::evict_copy_kernel<mla::kDRow> : mla::evict_copy_kernel<2 * mla::kDRow>,
+                        dim3((keep + mla::kEvRows - 1) / mla::kEvRows, batch), dim3(256), 0, s, src, dst,
+                        static_cast<const int32_t*>(kept), ws, keep, capacity_out, weights_out, lens_out);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_evict_workspace_size(int32_t batch, int32_t keep) {
+  if (batch <= 0 || keep <= 0) return 0;
+  return mla::ev_ws_bytes(batch, keep);
+}
+
+mla_status mla_cache_evict(const mla_bf16* cache, const int32_t* block_table, const int32_t* seq_lens,
+                           const float* weights, mla_cache_desc desc, int32_t batch, int32_t keep, int32_t sinks,
+                           int32_t recent, mla_bf16* cache_out, const int32_t* block_table_out,
+                           mla_cache_desc desc_out, int32_t* kept, int32_t* lens_out, float* weights_out,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  return launch_evict(cache, nullptr, block_table, seq_lens, weights, desc, batch, keep, sinks, recent, cache_out,
+                      nullptr, block_table_out, desc_out, kept, lens_out, weights_out, workspace, workspace_bytes,
+                      stream);
+}
+
+mla_status mla_cache_evict_fp8(const uint8_t* cache, const uint8_t* scales, const int32_t* block_table,
+                               const int32_t* seq_lens, const float* weights, mla_cache_desc desc, int32_t batch,
+                               int32_t keep, int32_t sinks, int32_t recent, uint8_t* cache_out, uint8_t* scales_out,
+                               const int32_t* block_table_out, mla_cache_desc desc_out, int32_t* kept,
+                               int32_t* lens_out, float* weights_out, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (scales == nullptr || scales_out == nullptr) return MLA_ERR_INVALID_ARG;
+  return launch_evict(cache, scales, block_table, seq_lens, weights, desc, batch, keep, sinks, recent, cache_out,
+                      scales_out, block_table_out, desc_out, kept, lens_out, weights_out, workspace, workspace_bytes,
+                      stream);
 }
 
 }  // extern "C"

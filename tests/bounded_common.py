@@ -100,6 +100,6 @@ class RowCache:
     def rows_of(self, b, t):
         t = np.asarray(t)
         if not self.paged:
-            return torch.from_numpy(b * self.stride + t)
+            return torch.as_tensor(b * self.stride + t)
         table = self.table.cpu().numpy()
-        return torch.from_numpy(table[b, t // 64].astype(np.int64) * 64 + t % 64)
+        return torch.as_tensor(table[b, t // 64].astype(np.int64) * 64 + t % 64)
