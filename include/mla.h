@@ -291,7 +291,43 @@ mla_status mla_prefill_attn_window(const mla_bf16* q_full, const mla_bf16* cache
 int32_t mla_window_span(int32_t max_seq_len, int32_t window, int32_t sinks);
 
 /*
- * (8) Eviction from the cache by accumulated attention weight (the pages have no counterpart).
+ * (8) Attention weight accumulated per cached token (the pages have no counterpart): how much the query
+ *     rows looked at each token, over all 128 heads.  For every sequence b and t < seq_lens[b]
+ *         weights[b * capacity + t] = decay * prev[b * capacity + t]
+ *                                   + sum_i sum_h exp(softmax_scale * q_full[i, h] . row(b, t) - lse[i, h])
+ * with lse as the attention call over the same rows, queries and scale wrote it: the terms of one row
+ * then sum to 128 over its tokens.  Elements at t >= seq_lens[b] are left as they were.
+ *   mla_attn_weights(_fp8), after mla_decode_attn(_fp8): one row per sequence, i = b.
+ *   mla_prefill_attn_weights, after mla_prefill_attn: the rows of sequence b are q_start[b] <= i <
+ *     q_start[b + 1], and row i counts for t < q_len[i].  A sequence without rows: decay * prev.
+ * Products in fp32 (exact for bf16), sums and exponentials in fp32; the same bits on every call.
+ *   q_full [rows, 128, 576] bf16   lse [rows, 128] fp32 (a head whose lse is -inf adds nothing)
+ *   prev   [batch, capacity] fp32, or NULL (taken as 0); weights may be prev
+ *   decay  >= 0, finite            weights [batch, capacity] fp32, capacity = max_seq_len or
+ *                                  max_blocks_per_seq * 64
+ *   q_start [batch + 1] int32, ascending from 0 on, at most n_queries   q_len [n_queries] int32
+ *   workspace (mla_prefill_attn_weights) >= mla_prefill_attn_weights_workspace_size(batch, capacity,
+ *     n_queries) bytes, 16-byte aligned, its contents need not be initialised
+ * batch and n_queries <= 16384 (MLA_ERR_UNSUPPORTED).  A length outside [0, capacity] is clamped, a pair
+ * of q_start entries that descends or leaves [0, n_queries] counts as no rows (MLA_DEVERR_SEQLEN_RANGE
+ * both); rows of a bad block id read as zeros (MLA_DEVERR_BLOCK_RANGE).
+ */
+mla_status mla_attn_weights(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                            const int32_t* seq_lens, mla_cache_desc desc, int32_t batch, float softmax_scale,
+                            const float* lse, const float* prev, float decay, float* weights, void* stream);
+mla_status mla_attn_weights_fp8(const mla_bf16* q_full, const uint8_t* cache, const uint8_t* scales,
+                                const int32_t* block_table, const int32_t* seq_lens, mla_cache_desc desc,
+                                int32_t batch, float softmax_scale, const float* lse, const float* prev, float decay,
+                                float* weights, void* stream);
+size_t mla_prefill_attn_weights_workspace_size(int32_t batch, int32_t max_seq_len, int32_t n_queries);
+mla_status mla_prefill_attn_weights(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                                    const int32_t* seq_lens, const int32_t* q_start, const int32_t* q_len,
+                                    mla_cache_desc desc, int32_t batch, int32_t n_queries, float softmax_scale,
+                                    const float* lse, const float* prev, float decay, void* workspace,
+                                    size_t workspace_bytes, float* weights, void* stream);
+
+/*
+ * (9) Eviction from the cache by accumulated attention weight (the pages have no counterpart).
  * Sequence b holds L = seq_lens[b] tokens of weights weights[b * capacity + t].  If L <= keep it keeps
  * them all.  Otherwise it keeps its first `sinks`, its last `recent` and, of those between, the
  * keep - sinks - recent with the largest weights; equal weights (0 and -0 among them) go to the lower

@@ -70,6 +70,11 @@ def _load():
         "mla_window_span": (I32, [I32, I32, I32]),
         "mla_cache_append_at": (ctypes.c_int, [P, P, P, P, P, P, P, CacheDesc, I32, F32, P]),
         "mla_cache_append_at_fp8": (ctypes.c_int, [P, P, P, P, P, P, P, P, CacheDesc, I32, F32, P]),
+        "mla_attn_weights": (ctypes.c_int, [P, P, P, P, CacheDesc, I32, F32, P, P, F32, P, P]),
+        "mla_attn_weights_fp8": (ctypes.c_int, [P, P, P, P, P, CacheDesc, I32, F32, P, P, F32, P, P]),
+        "mla_prefill_attn_weights_workspace_size": (SZ, [I32, I32, I32]),
+        "mla_prefill_attn_weights": (ctypes.c_int, [P, P, P, P, P, P, CacheDesc, I32, I32, F32, P, P, F32, P, SZ, P,
+                                                    P]),
         "mla_evict_workspace_size": (SZ, [I32, I32]),
         "mla_cache_evict": (ctypes.c_int, [P, P, P, P, CacheDesc, I32, I32, I32, I32, P, P, CacheDesc, P, P, P, P, SZ,
                                            P]),
@@ -263,6 +268,44 @@ def prefill_attn_window(q_full, cache, q_seq, q_len, desc: CacheDesc, workspace,
     _check(lib.mla_prefill_attn_window(_ptr(q_full), _ptr(cache), _ptr(block_table), _ptr(q_seq), _ptr(q_len), desc, n,
                                        window, sinks, softmax_scale, num_splits, _ptr(workspace), wb, _ptr(out_lat),
                                        _ptr(lse), _stream(stream)), "mla_prefill_attn_window")
+
+
+def attn_weights(q_full, cache, seq_lens, desc: CacheDesc, lse, weights, *, prev=None, decay: float = 1.0,
+                 block_table=None, softmax_scale: float = 1.0 / 192 ** 0.5, stream=None, batch: int | None = None):
+    """mla_attn_weights: weights[b, t] = decay * prev[b, t] + the attention weight of token t over the
+    heads of query row b, whose log-sum-exps lse decode_attn wrote (prev None: 0; weights may be prev)."""
+    b = q_full.shape[0] if batch is None else batch
+    _check(lib.mla_attn_weights(_ptr(q_full), _ptr(cache), _ptr(block_table), _ptr(seq_lens), desc, b, softmax_scale,
+                                _ptr(lse), _ptr(prev), decay, _ptr(weights), _stream(stream)), "mla_attn_weights")
+
+
+def attn_weights_fp8(q_full, cache, scales, seq_lens, desc: CacheDesc, lse, weights, *, prev=None, decay: float = 1.0,
+                     block_table=None, softmax_scale: float = 1.0 / 192 ** 0.5, stream=None,
+                     batch: int | None = None):
+    """mla_attn_weights_fp8: attn_weights over an FP8 cache."""
+    b = q_full.shape[0] if batch is None else batch
+    _check(lib.mla_attn_weights_fp8(_ptr(q_full), _ptr(cache), _ptr(scales), _ptr(block_table), _ptr(seq_lens), desc, b,
+                                    softmax_scale, _ptr(lse), _ptr(prev), decay, _ptr(weights), _stream(stream)),
+           "mla_attn_weights_fp8")
+
+
+def prefill_attn_weights_workspace_size(batch: int, max_seq_len: int, n_queries: int) -> int:
+    return lib.mla_prefill_attn_weights_workspace_size(batch, max_seq_len, n_queries)
+
+
+def prefill_attn_weights(q_full, cache, seq_lens, q_start, q_len, desc: CacheDesc, lse, workspace, weights, *,
+                         prev=None, decay: float = 1.0, block_table=None, softmax_scale: float = 1.0 / 192 ** 0.5,
+                         stream=None, batch: int | None = None, n_queries: int | None = None,
+                         workspace_bytes: int | None = None):
+    """mla_prefill_attn_weights: attn_weights with the rows q_start[b] .. q_start[b + 1] - 1 of sequence b,
+    row i counting for its first q_len[i] tokens."""
+    b = seq_lens.shape[0] if batch is None else batch
+    n = q_full.shape[0] if n_queries is None else n_queries
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(lib.mla_prefill_attn_weights(_ptr(q_full), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(q_start),
+                                        _ptr(q_len), desc, b, n, softmax_scale, _ptr(lse), _ptr(prev), decay,
+                                        _ptr(workspace), wb, _ptr(weights), _stream(stream)),
+           "mla_prefill_attn_weights")
 
 
 def evict_workspace_size(batch: int, keep: int) -> int:

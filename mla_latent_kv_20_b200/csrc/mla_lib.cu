@@ -15,6 +15,7 @@
 
 #include "../../include/mla.h"
 #include "append.cuh"
+#include "attn_weights.cuh"
 #include "decode_common.cuh"
 #include "decode_tc.cuh"
 #include "down_proj.cuh"
@@ -544,6 +545,134 @@ mla_status mla_prefill_attn_window(const mla_bf16* q_full, const mla_bf16* cache
   const mla::WindowRows win{window, sinks};
   return launch_attn(q_full, cache, block_table, q_len, q_seq, desc, n_queries, softmax_scale, num_splits, workspace,
                      workspace_bytes, out_lat, lse, stream, nullptr, &win);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// Attention weights accumulated per cached token.
+// ------------------------------------------------------------------------------------------
+namespace {
+
+// 4-D view of a cache for boxes of `groups` 8-row groups x 3 dim-slabs, laid out [group][slab][8 rows]
+// [64 elements] (the tile layout of attn_weights.cuh).  Grouped: (element, row of the group, slab, group),
+// where every sequence starts at a multiple of 8 rows; otherwise (element, row, slab), a group per copy.
+bool make_map_groups(CUtensorMap* map, const void* base, uint64_t rows, bool fp8, bool grouped) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t e = fp8 ? 1 : 2;
+  const cuuint64_t dims[4] = {64, grouped ? 8 : rows, 9, grouped ? rows / 8 : 1};
+  const cuuint64_t strides[3] = {mla::kDRow * e, 64 * e, 8 * mla::kDRow * e};
+  const cuuint32_t box[4] = {64, 8, mla::kAwSlabs, grouped ? 8u : 1u};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Work ranges: as many as CTA pairs are resident, at most one per unit (256 tokens x a query row).
+int attn_weights_ranges(int batch, int max_seq_len, int n_queries) {
+  const double units = static_cast<double>(batch) * ((max_seq_len - 1) / mla::kAwTile + 1) * std::max(n_queries, 1);
+  return static_cast<int>(std::min(units, static_cast<double>(std::min(decode_cluster_slots(), kMaxSplits))));
+}
+
+// rows < 0: a decode step, one query row per sequence.
+mla_status launch_attn_weights(const mla_bf16* q_full, const void* cache, const uint8_t* scales,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
+                               const int32_t* q_len, mla_cache_desc desc, int32_t batch, int32_t rows,
+                               float softmax_scale, const float* lse, const float* prev, float decay, void* workspace,
+                               size_t workspace_bytes, float* weights, void* stream) {
+  const bool chunk = rows >= 0, fp8 = scales != nullptr;
+  if (batch < 0 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
+  if (!(decay >= 0.f) || !std::isfinite(decay)) return MLA_ERR_INVALID_ARG;
+  if (batch > mla::kMaxDecodeBatch || rows > mla::kMaxDecodeBatch) return MLA_ERR_UNSUPPORTED;
+  CacheView v;
+  const mla_status st = check_cache(desc, cache, block_table, &v);
+  if (st != MLA_OK) return st;
+  if (batch > desc.num_seqs) return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (seq_lens == nullptr || weights == nullptr) return MLA_ERR_INVALID_ARG;
+  if (chunk && q_start == nullptr) return MLA_ERR_INVALID_ARG;
+  if (rows != 0) {
+    if (q_full == nullptr || lse == nullptr || (chunk && q_len == nullptr)) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_full) || !aligned16(lse)) return MLA_ERR_INVALID_ARG;
+  }
+  if (desc.num_rows >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
+  const int capacity = cache_capacity(desc);
+  const int P = attn_weights_ranges(batch, capacity, chunk ? rows : 1);
+  if (chunk && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < mla::aw_ws_bytes(P)))
+    return MLA_ERR_WORKSPACE;
+  mla::AwArgs a;
+  a.v = v;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.q_len = q_len;
+  a.n_rows = chunk ? rows : batch;
+  a.batch = batch;
+  a.capacity = capacity;
+  a.P = P;
+  a.grouped = desc.page_size != 0 || desc.max_seq_len % 8 == 0;
+  a.scale_log2 = softmax_scale * mla::kLog2e;
+  a.decay = decay;
+  a.lse = lse;
+  a.prev = prev;
+  a.weights = weights;
+  a.scales = scales;
+  a.part = static_cast<float*>(workspace);
+  a.rec = chunk ? reinterpret_cast<int4*>(a.part + static_cast<int64_t>(2 * P) * mla::kAwTile) : nullptr;
+  CUtensorMap tk, tq;
+  // (a chunk of no rows has no queries: the map is then not read)
+  if (!make_map_groups(&tk, cache, desc.num_rows, fp8, a.grouped) ||
+      !make_map_slabs(&tq, rows != 0 ? static_cast<const void*>(q_full) : cache,
+                      static_cast<uint64_t>(std::max(a.n_rows, 1)) * mla::kHeads, mla::kAwSlabs))
+    return MLA_ERR_CUDA;
+  auto kernel = chunk ? mla::attn_weights_kernel<true, false>
+                      : (fp8 ? mla::attn_weights_kernel<false, true> : mla::attn_weights_kernel<false, false>);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mla::kAwSmemBytes) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  cudaStream_t s = as_stream(stream);
+  const mla_status ls = launch_chained(kernel, dim3(2 * P), dim3(mla::aw_threads(fp8)),
+                                       static_cast<size_t>(mla::kAwSmemBytes), s, tk, tq, a);
+  if (ls != MLA_OK || !chunk) return ls;
+  return launch_chained(mla::attn_weights_join_kernel, dim3(P), dim3(mla::kAwTile), 0, s, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_attn_weights(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                            const int32_t* seq_lens, mla_cache_desc desc, int32_t batch, float softmax_scale,
+                            const float* lse, const float* prev, float decay, float* weights, void* stream) {
+  return launch_attn_weights(q_full, cache, nullptr, block_table, seq_lens, nullptr, nullptr, desc, batch, -1,
+                             softmax_scale, lse, prev, decay, nullptr, 0, weights, stream);
+}
+
+mla_status mla_attn_weights_fp8(const mla_bf16* q_full, const uint8_t* cache, const uint8_t* scales,
+                                const int32_t* block_table, const int32_t* seq_lens, mla_cache_desc desc,
+                                int32_t batch, float softmax_scale, const float* lse, const float* prev, float decay,
+                                float* weights, void* stream) {
+  if (scales == nullptr) return MLA_ERR_INVALID_ARG;
+  return launch_attn_weights(q_full, cache, scales, block_table, seq_lens, nullptr, nullptr, desc, batch, -1,
+                             softmax_scale, lse, prev, decay, nullptr, 0, weights, stream);
+}
+
+size_t mla_prefill_attn_weights_workspace_size(int32_t batch, int32_t max_seq_len, int32_t n_queries) {
+  if (batch <= 0 || max_seq_len <= 0 || n_queries < 0) return 0;
+  return mla::aw_ws_bytes(attn_weights_ranges(batch, max_seq_len, n_queries));
+}
+
+mla_status mla_prefill_attn_weights(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
+                                    const int32_t* seq_lens, const int32_t* q_start, const int32_t* q_len,
+                                    mla_cache_desc desc, int32_t batch, int32_t n_queries, float softmax_scale,
+                                    const float* lse, const float* prev, float decay, void* workspace,
+                                    size_t workspace_bytes, float* weights, void* stream) {
+  if (n_queries < 0) return MLA_ERR_INVALID_ARG;
+  return launch_attn_weights(q_full, cache, nullptr, block_table, seq_lens, q_start, q_len, desc, batch, n_queries,
+                             softmax_scale, lse, prev, decay, workspace, workspace_bytes, weights, stream);
 }
 
 }  // extern "C"

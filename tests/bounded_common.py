@@ -8,7 +8,9 @@ Bounds, from the arithmetic of the kernels (u = 2^-24, half a step of fp32):
   * out_lat: the weights' error times pc = sum_t p_t |c_t|, the weights' rounding to bf16 (half a
     step, 2^-8, relative) times pc, and the output's rounding to bf16, 2^-8 relative;
   * lse: ds plus the fp32 arithmetic around it, <= 2^-16;
-  * a sum of weights: each term within 2 ds + EXP, the additions of n terms within n * 2u of the sum.
+  * a sum of weights e^(s - l): each term within ds, and the fp32 argument of exp2: the factor scale log2(e)
+    within 3u, l log2(e) within 2u, the fused product within u, so (6u (|s| + |l|) log2(e)) ln 2 + 2^-21 of
+    exp2 itself, relative; the additions of n terms within n * 2u of the sum.
 """
 from __future__ import annotations
 
@@ -36,6 +38,16 @@ def assert_window_row(g_out, g_lse, ref):
     assert np.all(lerr <= ds + 2.0 ** -16), f"lse off by {lerr.max():.3e}"
 
 
+def weight_sums(q, rows, lse, scale=SCALE):
+    """(sum over heads of e^(s - lse) for each row, its error bound); q [H, 576], rows [L, 576], lse [H]."""
+    s = scale * (q @ rows.T)
+    l = np.where(np.isneginf(lse), np.inf, lse)[:, None]
+    w = np.exp(s - l)
+    rel = score_err(scale * (np.abs(q) @ np.abs(rows).T)) + 6 * U * (np.abs(s) + np.abs(np.where(np.isinf(l), 0, l))) + \
+        2.0 ** -21
+    return w.sum(axis=0), (w * rel).sum(axis=0) + len(q) * 2 * U * w.sum(axis=0) + 1e-35
+
+
 def f64(t: torch.Tensor) -> np.ndarray:
     return t.detach().cpu().double().numpy()
 
@@ -55,7 +67,8 @@ class RowCache:
     """A cache holding the given rows ([L_b, 576] bf16 CPU tensors), in pages or contiguous; every row
     and block-table entry no sequence uses holds NaN / -1.  fp8: rows coded by their oracle form."""
 
-    def __init__(self, m, seqs, paged, seed=0, max_len=None, fp8=False, device="cuda"):
+    def __init__(self, m, seqs, paged, seed=0, max_len=None, fp8=False, device="cuda",
+                 align=16):
         import oracle
         lens = [len(s) for s in seqs]
         B, L = len(seqs), max(max(lens + [1]) if max_len is None else max_len, 1)
@@ -72,7 +85,7 @@ class RowCache:
             self.desc = m.paged_desc(B, width, blocks)
             rows, self.table = blocks * 64, torch.from_numpy(table)
         else:
-            L = (L + 15) // 16 * 16
+            L = (L + align - 1) // align * align
             rows, self.table, self.desc = B * L, None, m.contiguous_desc(B, L)
         self.paged, self.stride, self.lens = paged, L, lens
         self.capacity = L if not paged else width * 64
