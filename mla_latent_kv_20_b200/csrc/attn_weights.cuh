@@ -37,38 +37,43 @@
 namespace mla {
 
 constexpr int kAwTile = 256;                       // tokens of a unit (128 per CTA)
-constexpr int kAwParts = 3;                        // parts of a K or Q buffer
+constexpr int kAwParts = 3;                        // parts of the K buffer
 constexpr int kAwSlabs = 9 / kAwParts;             // 64-dim slabs of a part
-constexpr int kAwQPart = kAwSlabs * kTcSlab;       // 64 heads x 3 slabs
+constexpr int kAwQParts = 3;                       // parts of the Q buffer
+constexpr int kAwQSlabs = 9 / kAwQParts;
+constexpr int kAwQPart = kAwQSlabs * kTcSlab;      // 64 heads
+static_assert(kAwQParts % kAwParts == 0, "a part of K covers whole parts of Q");
 constexpr int kAwKBox = 64 * kAwSlabs * 128;       // 64 tokens x 3 slabs
 constexpr int kAwKPart = 2 * kAwKBox;
 constexpr int kAwOffQ = 0;
-constexpr int kAwOffK = kAwOffQ + kAwParts * kAwQPart;
+constexpr int kAwOffK = kAwOffQ + kAwQParts * kAwQPart;
 constexpr int kAwOffLse = kAwOffK + kAwParts * kAwKPart;   // [2][128] -lse * log2(e)
 constexpr int kAwOffRed = kAwOffLse + 2 * kHeads * 4;      // [2][128] sums over the upper heads
 constexpr int kAwOffBar = kAwOffRed + 2 * 128 * 4;
-constexpr int kAwOffMisc = kAwOffBar + 256;
+constexpr int kAwOffMisc = kAwOffBar + 512;
 constexpr int kAwSmemBytes = kAwOffMisc + 64;
 static_assert(kAwSmemBytes <= 232448, "shared memory budget");
 
 constexpr int kAwSumWarps = 8;                     // read S, exponentiate, sum
-constexpr int kAwProducerWarp = 8;
-constexpr int kAwMmaWarp = 9;                      // and the next one
+constexpr int kAwMmaWarp = 8;                      // and the next one
+constexpr int kAwProducerWarp = 10;                // and, bf16, the next two
 constexpr int kAwConvWarp0 = 11;
 constexpr int kAwConvThreads = 256;
-constexpr int kAwThreads = 32 * kAwConvWarp0;
-__host__ __device__ constexpr int aw_threads(bool fp8) { return kAwThreads + (fp8 ? kAwConvThreads : 0); }
+__host__ __device__ constexpr int aw_producers(bool fp8) { return fp8 ? 1 : kAwParts; }
+__host__ __device__ constexpr int aw_threads(bool fp8) {
+  return 32 * (kAwProducerWarp + aw_producers(fp8)) + (fp8 ? kAwConvThreads : 0);
+}
 
 struct AwBars {
   uint64_t k_full[kAwParts];    // even CTA: both CTAs' part landed (one arrival per CTA + tx)
   uint64_t k_empty[kAwParts];   // both: the part consumed (one commit per issuer)
-  uint64_t q_full[kAwParts];
-  uint64_t q_empty[kAwParts];
+  uint64_t q_full[kAwQParts];
+  uint64_t q_empty[kAwQParts];
   uint64_t s_full[2];           // both: a unit's scores done (one commit per issuer)
   uint64_t s_empty[2];          // even CTA: every summing warp of both CTAs has read them
   uint64_t kraw[kAwParts];      // FP8, per CTA: the part's codes landed (+ tx)
 };
-static_assert(sizeof(AwBars) <= 256, "barrier block");
+static_assert(sizeof(AwBars) <= 512, "barrier block");
 
 struct AwArgs {
   CacheView v;
@@ -209,11 +214,14 @@ struct AwCursor {
   }
 };
 
-// ------------------------------------------------------------------------------ TMA producer (one warp)
+// ------------------------------------------------------------------------------ TMA producers
+// A thread needs about 0.27 us to wait for a slot, announce the bytes and issue the copy, whatever its size
+// (8 KB copies from L2: 30 GB/s per SM from one thread, 111 from four), so a chunk's queries, 9 copies per 1.2 us
+// of MMAs, take three producer warps: warp i copies part i of K and the parts of Q that it covers.
 template <bool kRows, bool kFp8>
 __device__ bool aw_producer(const CUtensorMap* tm_k, const CUtensorMap* tm_q, const AwArgs& a, const AwPlan& plan,
-                            uint8_t* smem, AwBars* bars, int rank, volatile int* abort_flag) {
-  if ((threadIdx.x & 31) != 0) return true;   // one lane issues
+                            uint8_t* smem, AwBars* bars, int rank, int me, volatile int* abort_flag) {
+  if (!elect_one()) return true;
   AwCursor<kRows> cur(a, plan);
   uint32_t kl = 0, ql = 0;   // tiles and query rows loaded
   int held = -1;             // the query row in shared memory
@@ -232,7 +240,7 @@ __device__ bool aw_producer(const CUtensorMap* tm_k, const CUtensorMap* tm_q, co
       const int q = cur.s.q0 + r;
       const bool new_q = q != held;
 #pragma unroll 1
-      for (int p = 0; p < kAwParts; ++p) {
+      for (int p = me; p < kAwParts; p += aw_producers(kFp8)) {
         if (first) {
           if (kl > 0 && !wait(&bars->k_empty[p], (kl - 1) & 1u, 0x40 + p)) return false;
           uint64_t* kraw = &bars->kraw[p];
@@ -263,13 +271,16 @@ __device__ bool aw_producer(const CUtensorMap* tm_k, const CUtensorMap* tm_q, co
           }
         }
         if (new_q) {
-          if (ql > 0 && !wait(&bars->q_empty[p], (ql - 1) & 1u, 0x44 + p)) return false;
-          const uint32_t full = lbar(&bars->q_full[p]);
-          if (rank == 0)
-            mbar_arrive_expect_tx_relaxed(full, 2u * kAwQPart);
-          else
-            mbar_arrive_relaxed(full);
-          tma_load_3d_pair(smem + kAwOffQ + p * kAwQPart, tm_q, full, 0, q * kHeads + 64 * rank, kAwSlabs * p);
+#pragma unroll 1
+          for (int i = p * (kAwQParts / kAwParts); i < (p + 1) * (kAwQParts / kAwParts); ++i) {
+            if (ql > 0 && !wait(&bars->q_empty[i], (ql - 1) & 1u, 0x44)) return false;
+            const uint32_t full = lbar(&bars->q_full[i]);
+            if (rank == 0)
+              mbar_arrive_expect_tx_relaxed(full, 2u * kAwQPart);
+            else
+              mbar_arrive_relaxed(full);
+            tma_load_3d_pair(smem + kAwOffQ + i * kAwQPart, tm_q, full, 0, q * kHeads + 64 * rank, kAwQSlabs * i);
+          }
         }
       }
       if (first) ++kl;
@@ -302,24 +313,23 @@ __device__ bool aw_mma(uint8_t* smem, AwBars* bars, uint32_t tmem, int j, const 
       const int nr = cur.active(r + 1);
       const bool last = nr >= cur.r1;
       if (new_q && !q_freed)
-        for (int p = 0; p < kAwParts; ++p) umma_commit_pair_mc(&bars->q_empty[p], 3);
+        for (int i = 0; i < kAwQParts; ++i) umma_commit_pair_mc(&bars->q_empty[i], 3);
       // S buffer u & 1 last held unit u - 2
       if (u >= 2 && !mbar_wait_cluster(&bars->s_empty[u & 1], ((u - 2) >> 1) & 1u, 0x50)) return false;
       const uint32_t d = tmem + 256 * j + 128 * (u & 1);
 #pragma unroll
-      for (int p = 0; p < kAwParts; ++p) {
-        if (first && !mbar_wait_cluster(&bars->k_full[p], kl & 1u, 0x51)) return false;
-        if (new_q && !mbar_wait_cluster(&bars->q_full[p], ql & 1u, 0x52)) return false;
-        tc_fence_after();
+      for (int c = 0; c < 9; ++c) {   // dim-slabs
+        const int p = c / kAwSlabs, i = c / kAwQSlabs;
+        const bool new_part = c % kAwSlabs == 0, new_q_part = c % kAwQSlabs == 0;
+        if (first && new_part && !mbar_wait_cluster(&bars->k_full[p], kl & 1u, 0x51)) return false;
+        if (new_q && new_q_part && !mbar_wait_cluster(&bars->q_full[i], ql & 1u, 0x52)) return false;
+        if (new_part || new_q_part) tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < kAwSlabs; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; kk += 2)
-            umma_bf16_pair(d, sdesc_add(dk, p * kAwKPart + c * 1024 + 32 * (kk + j)),
-                           sdesc_add(dq, p * kAwQPart + c * kTcSlab + 32 * (kk + j)), idesc,
-                           (p | c | kk) != 0 ? 1u : 0u);
-        if (last) umma_commit_pair_mc(&bars->k_empty[p], 3);
-        if (!last) umma_commit_pair_mc(&bars->q_empty[p], 3);
+        for (int kk = 0; kk < 4; kk += 2)
+          umma_bf16_pair(d, sdesc_add(dk, p * kAwKPart + (c % kAwSlabs) * 1024 + 32 * (kk + j)),
+                         sdesc_add(dq, c * kTcSlab + 32 * (kk + j)), idesc, (c | kk) != 0 ? 1u : 0u);
+        if (last && (c + 1) % kAwSlabs == 0) umma_commit_pair_mc(&bars->k_empty[p], 3);
+        if (!last && (c + 1) % kAwQSlabs == 0) umma_commit_pair_mc(&bars->q_empty[i], 3);
       }
       umma_commit_pair_mc(&bars->s_full[u & 1], 3);
       if (first) ++kl;
@@ -501,9 +511,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(aw_threads(kFp8), 1)
     for (int p = 0; p < kAwParts; ++p) {
       mbar_init(&bars->k_full[p], 2);
       mbar_init(&bars->k_empty[p], 2);
-      mbar_init(&bars->q_full[p], 2);
-      mbar_init(&bars->q_empty[p], 2);
       mbar_init(&bars->kraw[p], 1);
+    }
+    for (int i = 0; i < kAwQParts; ++i) {
+      mbar_init(&bars->q_full[i], 2);
+      mbar_init(&bars->q_empty[i], 2);
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(&bars->s_full[j], 2);
@@ -534,11 +546,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(aw_threads(kFp8), 1)
   const uint32_t tmem = *tmem_slot;
   if (warp < kAwSumWarps) {
     aw_sum<kRows, kFp8>(a, pl, pair, smem, bars, tmem, rank, abort_flag);
-  } else if (warp == kAwProducerWarp) {
-    if (!aw_producer<kRows, kFp8>(&tm_k, &tm_q, a, pl, smem, bars, rank, abort_flag)) *abort_flag = 1;
+  } else if (warp >= kAwProducerWarp && warp < kAwProducerWarp + aw_producers(kFp8)) {
+    if (!aw_producer<kRows, kFp8>(&tm_k, &tm_q, a, pl, smem, bars, rank, warp - kAwProducerWarp, abort_flag))
+      *abort_flag = 1;
   } else if (kFp8 && warp >= kAwConvWarp0) {
     if (!aw_convert<kRows>(a, pl, smem, bars, abort_flag) && threadIdx.x == 32 * kAwConvWarp0) *abort_flag = 1;
-  } else if (rank == 0 && (threadIdx.x & 31) == 0) {
+  } else if (rank == 0 && elect_one()) {
     if (!aw_mma<kRows>(smem, bars, tmem, warp - kAwMmaWarp, a, pl, abort_flag)) *abort_flag = 1;
   }
   __syncwarp();

@@ -94,9 +94,10 @@ constexpr int kTcMmaWarp = 9;     // TMEM allocation (both CTAs); QK^T even K st
 constexpr int kTcPvWarp = 10;     // PV issue, first latent half (even CTA)
 constexpr int kTcMmaBWarp = 11;   // QK^T odd K steps (even CTA)
 constexpr int kTcPv1Warp = 12;    // PV issue, second latent half (even CTA)
-constexpr int kTcThreads = 32 * (kTcSoftmaxWarps + 5);
+constexpr int kTcVProducerWarp = 13;
+constexpr int kTcThreads = 32 * (kTcSoftmaxWarps + 6);
 // FP8 cache: four converter warps after the others.
-constexpr int kTcConvWarp0 = kTcSoftmaxWarps + 5;
+constexpr int kTcConvWarp0 = kTcSoftmaxWarps + 6;
 constexpr int kTcConvThreads = 128;
 constexpr int kTcThreadsFp8 = kTcThreads + kTcConvThreads;
 __host__ __device__ constexpr int tc_threads(bool fp8) { return fp8 ? kTcThreadsFp8 : kTcThreads; }
@@ -301,19 +302,19 @@ __device__ __noinline__ bool tc_load_ragged_v(uint8_t* box, const CUtensorMap* t
   return true;
 }
 
-template <bool kMapped, bool kFp8, class Rows>
+template <bool kV, bool kMapped, bool kFp8, class Rows>
 __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, const CUtensorMap* tm_v,
                             const CUtensorMap* tm_q, const CUtensorMap* tm_sc, const DecodeTcArgs& a,
                             const TcPlan& plan, uint8_t* smem, TcBars* bars, uint32_t rank, int pair,
                             volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
-  const bool l0 = lane == 0;
+  const bool l0 = elect_one();
   const bool leader = rank == 0;
   // Lane 0 waits; the verdict (and an abort seen meanwhile) is shared with the warp.
   auto wait0 = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
     int ok = 1;
     if (l0) ok = (mbar_wait(bar, parity, site) && !*abort_flag) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    return __all_sync(0xffffffffu, ok);
   };
   SegmentCursor cur{plan.b0, plan.off0, plan.start, plan.end, plan.b_end, pair, true, plan.len0};
   Segment sg;
@@ -331,11 +332,11 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
     // Q of sequence b.  The buffer is free once both QK^T parts have finished the previous segment.
     // Arrivals on the even CTA's barriers that only count (the data and its visibility come with
     // the TMA's complete_tx) are relaxed.
-    if (k > 0 && !wait0(&bars->q_empty, static_cast<uint32_t>(k - 1) & 1u, 0x14)) {
+    if (!kV && k > 0 && !wait0(&bars->q_empty, static_cast<uint32_t>(k - 1) & 1u, 0x14)) {
       ok = false;
       break;
     }
-    if (l0) {
+    if (!kV && l0) {
       tma_load_3d_pair(smem + kTcOffQ, tm_q, lbar(&bars->q_full), 0, b * kHeads + 64 * static_cast<int>(rank), 0);
       if (leader)
         mbar_arrive_expect_tx_relaxed(lbar(&bars->q_full), 2u * kTcQBytes);
@@ -344,7 +345,7 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
     }
     // TMA row of token t of query row b's sequence (a fully out-of-bounds box for a bad map entry).
     // Every lane calls it (the paged lookup shares the block ids across the warp).
-    const int cb = tc_cache_seq<kMapped>(a, b, true);
+    const int cb = tc_cache_seq<kMapped>(a, b, !kV);
     auto row_of = [&](int t) -> int {
       if (kMapped && cb < 0) return -kTcTile;
       if (!paged) return tma_row(a.v, cb, map.real(t));
@@ -427,10 +428,7 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
     // K(i) then V(i - 1): one call site each (the loop runs one step past the last K).  (Paged rows
     // pulled into L2 two tiles ahead by this warp's lanes measured slower: 211 -> 232 us for the
     // batch-128 paged workload, A/B on identical inputs.)
-    for (int i = 0; ok && i <= n_tiles; ++i) {
-      if (i < n_tiles) ok = issue_k(i);
-      if (i > 0 && ok) ok = issue_v(i - 1);
-    }
+    for (int i = 0; ok && i < n_tiles; ++i) ok = kV ? issue_v(i) : issue_k(i);
     g += n_tiles;
     ++k;
   }
@@ -1221,15 +1219,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
     // an idle range: only the teardown below
   } else if (warp < kTcSoftmaxWarps) {
     tc_softmax<kMapped, Rows>(a, pl, pair, smem, bars, red, tmem, rank, abort_flag);
-  } else if (warp == kTcProducerWarp) {
-    if (!tc_producer<kMapped, kFp8, Rows>(&tm_ka, &tm_kb, &tm_v, &tm_q, &tm_sc, a, pl, smem, bars, rank, pair,
-                                    abort_flag) &&
-        (threadIdx.x & 31) == 0)
-      *abort_flag = 1;
+  } else if (warp == kTcProducerWarp || warp == kTcVProducerWarp) {
+    const bool ok = warp == kTcProducerWarp
+                        ? tc_producer<false, kMapped, kFp8, Rows>(&tm_ka, &tm_kb, &tm_v, &tm_q, &tm_sc, a, pl, smem,
+                                                                  bars, rank, pair, abort_flag)
+                        : tc_producer<true, kMapped, kFp8, Rows>(&tm_ka, &tm_kb, &tm_v, &tm_q, &tm_sc, a, pl, smem,
+                                                                 bars, rank, pair, abort_flag);
+    if (!ok && (threadIdx.x & 31) == 0) *abort_flag = 1;
   } else if (kFp8 && warp >= kTcConvWarp0) {
     if (!tc_convert<Rows>(a, pl, pair, smem, bars, abort_flag) && threadIdx.x == 32 * kTcConvWarp0)
       *abort_flag = 1;
-  } else if (rank == 0 && (threadIdx.x & 31) == 0) {
+  } else if (rank == 0 && elect_one()) {
     bool ok = true;
     // One out-of-line copy of each issuer serves both of its warps (part / latent half as argument).
     const SegmentCursor cur{pl.b0, pl.off0, pl.start, pl.end, pl.b_end, pair, true, pl.len0};

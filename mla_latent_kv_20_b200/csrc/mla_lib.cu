@@ -627,7 +627,7 @@ mla_status launch_attn_weights(const mla_bf16* q_full, const void* cache, const 
   // (a chunk of no rows has no queries: the map is then not read)
   if (!make_map_groups(&tk, cache, desc.num_rows, fp8, a.grouped) ||
       !make_map_slabs(&tq, rows != 0 ? static_cast<const void*>(q_full) : cache,
-                      static_cast<uint64_t>(std::max(a.n_rows, 1)) * mla::kHeads, mla::kAwSlabs))
+                      static_cast<uint64_t>(std::max(a.n_rows, 1)) * mla::kHeads, mla::kAwQSlabs))
     return MLA_ERR_CUDA;
   auto kernel = chunk ? mla::attn_weights_kernel<true, false>
                       : (fp8 ? mla::attn_weights_kernel<false, true> : mla::attn_weights_kernel<false, false>);

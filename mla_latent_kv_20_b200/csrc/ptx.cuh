@@ -231,6 +231,17 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
 }
 
+// One lane of the (converged) warp.  The compiler knows that a branch on it leaves one thread, and keeps
+// the operands of tcgen05 and bulk-copy instructions in uniform registers; behind a branch on the lane
+// number it moves them there for each instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
