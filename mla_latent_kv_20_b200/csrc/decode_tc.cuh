@@ -142,7 +142,7 @@ struct TcBars {
   uint64_t k_empty[2];           // both CTAs, per part: K box consumed by the MMAs (one commit per QK^T issuer)
   uint64_t v_full[kTcVSlots];    // even CTA only: both CTAs' V box landed (one arrival per CTA + tx)
   uint64_t v_empty[kTcVSlots];   // both CTAs: V box consumed (one commit per PV warp)
-  uint64_t fix;                  // per CTA: local load of a ragged V box
+  uint64_t fix[kTcVSlots];       // per CTA and slot: local load of a ragged V box
   uint64_t s_full[2];            // both: QK^T of a tile done (one commit per part)
   uint64_t s_empty[2];           // even CTA only: every softmax warp of both CTAs has read S
   uint64_t p_full;               // even CTA only: P (and corrected O) of a tile ready in both CTAs
@@ -257,6 +257,7 @@ __device__ __forceinline__ void tma_load_4d_local(void* dst, const CUtensorMap* 
 __device__ __forceinline__ void zero_v_rows(uint8_t* box, int v0, int v1, int lane) {
   // each row is 4 slabs x 128 bytes: one 16-byte chunk per lane
   uint4* p = reinterpret_cast<uint4*>(box + (lane >> 3) * kTcSlab) + (lane & 7);
+#pragma unroll 8
   for (int row = v0; row < v1; ++row) p[row * 8] = make_uint4(0, 0, 0, 0);
 }
 
@@ -269,26 +270,18 @@ __device__ __forceinline__ void tc_box_hole(const Map& map, int tok0, int& h0, i
   h1 = min(max(map.hole1() - r0, 0), 64);
 }
 
-// A V box that reaches past the segment end, or (kHoles) holds hidden rows [h0, h1): loaded through
-// a CTA-local barrier (if any row is valid), those rows zeroed by all lanes after the copy has
-// landed, then published: each lane's proxy fence, the warp barrier, and lane 0's arrival with
-// release semantics on the even CTA's v_full.  Out of line: it runs at most twice per segment (four
-// times with a window).  False if a wait failed.
+// A V box that reaches past the segment end, or (kHoles) holds hidden rows [h0, h1), is loaded through
+// a CTA-local barrier of its slot; once the copy has landed all lanes zero those rows, and the box is
+// published: each lane's proxy fence, the warp barrier, and lane 0's arrival with release semantics on
+// the even CTA's v_full.  Out of line: it runs at most twice per segment (four times with a window).
+// False if the wait failed.
 template <bool kHoles>
-__device__ __noinline__ bool tc_load_ragged_v(uint8_t* box, const CUtensorMap* tm_v, uint64_t* fix, uint32_t fix_phase,
-                                              int row, int rank, int vcount, int h0, int h1, uint32_t vfull,
-                                              volatile int* abort_flag) {
+__device__ __noinline__ bool tc_finish_ragged_v(uint8_t* box, uint64_t* fix, uint32_t fix_phase, int rank, int vcount,
+                                                int h0, int h1, uint32_t vfull, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
-  if (vcount > 0) {
-    int ok = 1;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(fix, kTcVBox);
-      tma_load_4d_local(box, tm_v, fix, 0, row, 2 * rank, 0);
-      ok = (mbar_wait(fix, fix_phase, 0x13) && !*abort_flag) ? 1 : 0;
-    }
-    if (__shfl_sync(0xffffffffu, ok, 0) == 0) return false;
-  }
-  __syncwarp();
+  int ok = 1;
+  if (lane == 0) ok = (mbar_wait(fix, fix_phase, 0x13) && !*abort_flag) ? 1 : 0;
+  if (__shfl_sync(0xffffffffu, ok, 0) == 0) return false;
   if (kHoles) zero_v_rows(box, h0, h1, lane);
   zero_v_rows(box, vcount, 64, lane);
   fence_proxy_async_smem();
@@ -380,16 +373,14 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
       return true;
     };
     auto issue_v = [&](int i) -> bool {
-      // The V ring doubles as the epilogue's staging buffer: the first box of a segment waits
-      // until the previous segment's epilogue (in both CTAs) is done with it.
-      if (i == 0 && k > 0 && !wait0(&bars->o_free, static_cast<uint32_t>(k - 1) & 1u, 0x15)) return false;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h, ++vn) {
-        const int s = vn % kTcVSlots;
+      int v0[2], vh0[2], vh1[2];   // ragged boxes: valid rows, hidden rows
+      bool ragged[2] = {false, false};
+#pragma unroll
+      for (int s = 0; s < 2; ++s, ++vn) {   // box h of a tile sits in slot h
         if (vn >= kTcVSlots && !wait0(&bars->v_empty[s], static_cast<uint32_t>((vn / kTcVSlots) - 1) & 1u, 0x12))
           return false;
         uint8_t* box = smem + kTcOffV + s * kTcVBox;
-        const int tok0 = t_begin + i * kTcTile + 64 * h;
+        const int tok0 = t_begin + i * kTcTile + 64 * s;
         const int vcount = min(max(t_end - tok0, 0), 64);
         const int row = vcount > 0 ? row_of(tok0) : 0;
         if constexpr (kFp8) {
@@ -408,7 +399,9 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
         }
         int h0 = 0, h1 = 0;
         if (Rows::kHoles) tc_box_hole(map, tok0, h0, h1);
-        if (vcount == 64 && h0 == h1) {
+        if (vcount == 0) {   // no token: PV skips the box, its barrier completes on the arrivals alone
+          if (l0) mbar_arrive_relaxed(lbar(&bars->v_full[s]));
+        } else if (vcount == 64 && h0 == h1) {
           if (l0) {
             tma_load_4d_pair(box, tm_v, lbar(&bars->v_full[s]), 0, row, 2 * static_cast<int>(rank), 0);
             if (leader)
@@ -417,17 +410,27 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
               mbar_arrive_relaxed(lbar(&bars->v_full[s]));
           }
         } else {
-          if (!tc_load_ragged_v<Rows::kHoles>(box, tm_v, &bars->fix, fix_phase, row, static_cast<int>(rank), vcount,
-                                              h0, h1, lbar(&bars->v_full[s]), abort_flag))
-            return false;
-          if (vcount > 0) fix_phase ^= 1u;
+          if (l0) {
+            mbar_arrive_expect_tx(&bars->fix[s], kTcVBox);
+            tma_load_4d_local(box, tm_v, &bars->fix[s], 0, row, 2 * static_cast<int>(rank), 0);
+          }
+          ragged[s] = true;
+          v0[s] = vcount;
+          vh0[s] = h0;
+          vh1[s] = h1;
         }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {   // with both copies on their way
+        if (!ragged[s]) continue;
+        if (!tc_finish_ragged_v<Rows::kHoles>(smem + kTcOffV + s * kTcVBox, &bars->fix[s], (fix_phase >> s) & 1u,
+                                              static_cast<int>(rank), v0[s], vh0[s], vh1[s],
+                                              lbar(&bars->v_full[s]), abort_flag))
+          return false;
+        fix_phase ^= 1u << s;
       }
       return true;
     };
-    // K(i) then V(i - 1): one call site each (the loop runs one step past the last K).  (Paged rows
-    // pulled into L2 two tiles ahead by this warp's lanes measured slower: 211 -> 232 us for the
-    // batch-128 paged workload, A/B on identical inputs.)
     for (int i = 0; ok && i < n_tiles; ++i) ok = kV ? issue_v(i) : issue_k(i);
     g += n_tiles;
     ++k;
@@ -527,10 +530,12 @@ __device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, int nh, co
         tc_fence_after();
         const uint64_t pb = sdesc_add(dp, h * kTcSlab);
         const uint64_t vb = sdesc_add(dv, vs * kTcVBox);
+        if (h == 0 || sg.tok_begin + i * kTcTile + 64 < sg.tok_end) {
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4)   // 16-token groups; the segment's first MMA overwrites O
           umma_bf16_pair(ocol, sdesc_add(pb, 32 * g4), sdesc_add(vb, g4 * 2048), idesc_pv,
                          (i > 0 || h > 0 || g4 > 0) ? 1u : 0u);
+        }
         umma_commit_pair_mc(&bars->v_empty[vs], 3);
       }
       if (!ok) break;
@@ -648,24 +653,24 @@ __device__ bool tc_convert(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   return ok;
 }
 
-// Each lane holds 128 bytes (w[0..31]) of its own row r = lane of a 32-row block whose rows lie
-// row_stride bytes apart from row0.  Written through a 4 KB per-warp staging buffer (16-byte
-// chunks XOR-swizzled by row, so both passes are free of bank conflicts beyond the 4 wavefronts
-// a 512-byte access needs), each global store instruction covers four whole 128-byte row
+// Each lane holds 64 bytes (w[0..15]) of its own row r = lane of a 32-row block whose rows lie
+// row_stride bytes apart from row0.  Written through a 2 KB per-warp staging buffer (16-byte
+// chunks XOR-swizzled by row pair, so neither pass meets bank conflicts beyond the 4 wavefronts
+// a 512-byte access needs), each global store instruction covers eight whole 64-byte row
 // segments instead of 32 scattered 16-byte pieces.
-__device__ __forceinline__ void store_rows_128b(uint8_t* stage, const uint32_t (&w)[32], uint8_t* row0,
-                                                size_t row_stride, int lane) {
+__device__ __forceinline__ void store_rows_64b(uint8_t* stage, const uint32_t* w, uint8_t* row0, size_t row_stride,
+                                               int lane) {
   __syncwarp();
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
         make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int row = 4 * j + (lane >> 3);
-    const int c = lane & 7;
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+  for (int j = 0; j < 4; ++j) {
+    const int row = 8 * j + (lane >> 2);
+    const int c = lane & 3;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
     *reinterpret_cast<uint4*>(row0 + row * row_stride + c * 16) = v;
   }
 }
@@ -724,9 +729,9 @@ __device__ __noinline__ void tc_write_segment(bool direct, void* row, float* m_o
   const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
   const int lat0 = 256 * ch + 128 * half;
   const uint32_t ocol = tmem + lane_base + kTcColO + 128 * ch;
-  // Every MMA and copy of the segment is done (o_final) and the producer holds the next
-  // segment's V copies until o_free: the V buffers give 4 KB of staging per warp.
-  uint8_t* stage = smem + kTcOffV + warp * 4096;
+  // PV has read the segment's last P (o_final), and the next P is written by these warps after
+  // their next barrier: the P buffer gives 2 KB of staging per warp.
+  uint8_t* stage = smem + kTcOffP + warp * 2048;
   if (direct) {
     const float inv = l_tot > 0.f ? 1.f / l_tot : 0.f;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(row) + lat0;
@@ -745,7 +750,8 @@ __device__ __noinline__ void tc_write_segment(bool direct, void* row, float* m_o
               __floats2bfloat162_rn(__uint_as_float(r[q][2 * e]) * inv, __uint_as_float(r[q][2 * e + 1]) * inv);
           w[8 * q + e] = *reinterpret_cast<uint32_t*>(&h2);
         }
-      store_rows_128b(stage, w, row0 + 128 * qb, static_cast<size_t>(kDLat) * 2, lane);
+      store_rows_64b(stage, w, row0 + 128 * qb, static_cast<size_t>(kDLat) * 2, lane);
+      store_rows_64b(stage, w + 16, row0 + 128 * qb + 64, static_cast<size_t>(kDLat) * 2, lane);
     }
     if (half == 0 && ch == 0 && m_or_lse != nullptr)
       *m_or_lse = l_tot > 0.f ? (m_used + log2f(l_tot)) * kLn2 : -INFINITY;
@@ -757,7 +763,8 @@ __device__ __noinline__ void tc_write_segment(bool direct, void* row, float* m_o
       tmem_ld16(ocol + 32 * qb, *reinterpret_cast<uint32_t(*)[16]>(&w[0]));
       tmem_ld16(ocol + 32 * qb + 16, *reinterpret_cast<uint32_t(*)[16]>(&w[16]));
       tmem_ld_wait();
-      store_rows_128b(stage, w, row0 + 128 * qb, static_cast<size_t>(kDLat) * 4, lane);
+      store_rows_64b(stage, w, row0 + 128 * qb, static_cast<size_t>(kDLat) * 4, lane);
+      store_rows_64b(stage, w + 16, row0 + 128 * qb + 64, static_cast<size_t>(kDLat) * 4, lane);
     }
     if (half == 0 && ch == 0) {
       *m_or_lse = m_used;
@@ -801,7 +808,34 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   int k = 0;   // segment index
   bool ok = true;
   const Rows rows = tc_rows<Rows>(a);
-  while (cur.next(a.seq_lens, a.capacity, rows, sg)) {
+  // The segment whose tiles are done but whose O has not been read.  Its epilogue runs once the next
+  // segment's first P is in registers, so that the wait for the last PV overlaps that softmax.
+  struct {
+    int b, slot;
+    bool direct;
+    float m, l;
+  } done = {};
+  // Every warp passes the same barriers.  free_buf: the sums exchange (a maxima buffer not in use).
+  auto epilogue = [&](int kd, float* rl) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_final, static_cast<uint32_t>(kd) & 1u, 0x33))) ok = false;
+    tc_fence_after();
+    rl[me] = done.l;
+    named_bar_sync(1, 256);
+    const float l_tot = (done.l + rl[me ^ 64]) + (rl[me ^ 128] + rl[me ^ 192]);
+    if (ok && !*abort_flag) {
+      const int64_t h = 64 * static_cast<int>(rank) + hl;
+      if (done.direct) {
+        const int64_t bh = static_cast<int64_t>(done.b) * kHeads + h;
+        tc_write_segment(true, a.out_lat + bh * kDLat, a.lse != nullptr ? a.lse + bh : nullptr, nullptr, smem, tmem,
+                         done.m, l_tot);
+      } else {
+        const int64_t ml = static_cast<int64_t>(done.slot) * kHeads + h;
+        tc_write_segment(false, a.ws.o + ml * kDLat, a.ws.m + ml, a.ws.l + ml, smem, tmem, done.m, l_tot);
+      }
+    }
+  };
+  bool more = cur.next(a.seq_lens, a.capacity, rows, sg);
+  while (more) {
   const auto map = rows.map(sg.len);
   const int t_begin = sg.tok_begin, t_end = sg.tok_end, n_tiles = sg.n_tiles;
   float m_used = -INFINITY;
@@ -891,8 +925,20 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       pk[e] = *reinterpret_cast<uint32_t*>(&h2);
     }
     // The P buffer is free once PV(g-1) has read it.  By parity this is unambiguous for the
-    // same reason: p_empty has completed g-1 or g phases.
-    if (g >= 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->p_empty, static_cast<uint32_t>(g - 1) & 1u, 0x32))) {
+    // same reason: p_empty has completed g-1 or g phases.  Between segments the epilogue waits for
+    // more (all of PV), reads O and stages it through the P buffer; the barrier then lets every
+    // warp write P, and both CTAs learn that O may be overwritten.
+    if (i == 0 && k > 0) {
+      epilogue(k - 1, red + (j ^ 1) * 256);
+      tc_fence_before();
+      named_bar_sync(1, 256);
+      if (!ok) break;
+      if (lane == 0) {
+        fence_release_smem_to_cluster();
+        mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 0));
+        mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 1));
+      }
+    } else if (g >= 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->p_empty, static_cast<uint32_t>(g - 1) & 1u, 0x32))) {
       ok = false;
       break;
     }
@@ -918,44 +964,19 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     if (i + kTcPfDist < n_tiles)
       tc_prefetch_tile<kMapped>(a, map, sg.b, t_begin + (i + kTcPfDist) * kTcTile + 64 * static_cast<int>(rank), t_end);
   }
-  // ---- epilogue of the segment (every warp passes the same barriers, also after a failure)
-  if (ok && !__all_sync(0xffffffffu, mbar_wait(&bars->o_final, static_cast<uint32_t>(k) & 1u, 0x33))) ok = false;
-  tc_fence_after();
-  float* rl = red + (g & 1) * 256;   // the maxima buffer the segment's last tile did not use
-  rl[me] = l_run;
-  named_bar_sync(1, 256);
-  const float l_tot = (l_run + rl[me ^ 64]) + (rl[me ^ 128] + rl[me ^ 192]);
-  const bool write = ok && !*abort_flag;
-  if (write) {
-    const int64_t h = 64 * static_cast<int>(rank) + hl;
-    if (sg.direct) {
-      const int64_t bh = static_cast<int64_t>(sg.b) * kHeads + h;
-      tc_write_segment(true, a.out_lat + bh * kDLat, a.lse != nullptr ? a.lse + bh : nullptr, nullptr, smem, tmem,
-                       m_used, l_tot);
-    } else {
-      const int64_t ml = static_cast<int64_t>(sg.slot) * kHeads + h;
-      tc_write_segment(false, a.ws.o + ml * kDLat, a.ws.m + ml, a.ws.l + ml, smem, tmem, m_used, l_tot);
-    }
-  }
   // Leave only on `ok`, which every softmax warp reaches at the same wait (they all wait on the
   // same barriers), never on the abort flag, which warps may read at different moments: a warp
-  // leaving alone would strand the others at the next named barrier.  After the range's last
-  // segment nobody waits for the release below (may_continue is the same in every warp and false
-  // only when no segment follows).
-  if (!ok || !cur.may_continue()) break;
-  // O has been read (tcgen05.wait::ld) and the staging buffer's reads are done: release both to
-  // the next segment in both CTAs.  The barrier also keeps the next segment's first tile from
-  // overwriting the sums exchange before every warp has read it.
-  tc_fence_before();
-  fence_proxy_async_smem();
-  named_bar_sync(1, 256);
-  if (lane == 0) {
-    fence_release_smem_to_cluster();
-    mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 0));
-    mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 1));
-  }
+  // leaving alone would strand the others at the next named barrier.
+  if (!ok) break;
+  done.b = sg.b;
+  done.slot = sg.slot;
+  done.direct = sg.direct;
+  done.m = m_used;
+  done.l = l_run;
   ++k;
+  more = cur.next(a.seq_lens, a.capacity, rows, sg);
   }
+  if (ok && k > 0) epilogue(k - 1, red + (g & 1) * 256);   // the buffer the last tile did not use
 }
 
 // ------------------------------------------------------------------------------ work plan
@@ -1162,8 +1183,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
     for (int s = 0; s < kTcVSlots; ++s) {
       mbar_init(&bars->v_full[s], 2);   // one arrival per CTA of the pair (plus the copies' bytes)
       mbar_init(&bars->v_empty[s], 2);   // one commit per PV warp
+      mbar_init(&bars->fix[s], 1);
     }
-    mbar_init(&bars->fix, 1);
     mbar_init(&bars->s_full[0], 2);   // one commit per QK^T part
     mbar_init(&bars->s_full[1], 2);
     mbar_init(&bars->s_empty[0], 2 * kTcSoftmaxWarps);   // every softmax warp of both CTAs
