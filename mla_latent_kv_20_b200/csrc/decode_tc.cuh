@@ -254,36 +254,57 @@ __device__ __forceinline__ void tma_load_4d_local(void* dst, const CUtensorMap* 
 //        (zeros); its scores are masked anyway.
 //  V(i): per 64-token half h of the tile, latent [256n + 128r, +128) for n = 0, 1 in one box,
 //        laid out [n][chunk][64 rows][128 B].
-__device__ __forceinline__ void zero_v_rows(uint8_t* box, int v0, int v1, int lane) {
-  // each row is 4 slabs x 128 bytes: one 16-byte chunk per lane
+//
+// Rows of a V box that PV must not see: those at or past `valid` (past the segment's end) and the
+// hidden ones [h0, h1).  PV works in groups of 16 tokens and leaves out groups with no row to see;
+// in the others such rows are zeroed.
+struct TcBox {
+  int valid, h0, h1;
+  __device__ bool whole() const { return valid == 64 && h0 >= h1; }
+  __device__ bool sees(int r) const { return r < valid && !(r >= h0 && r < h1); }
+  // Whether group q has a row to see: the first row of the group that is not hidden, or none.
+  __device__ bool group(int q) const {
+    int r = 16 * q;
+    if (r >= h0 && r < h1) r = h1;
+    return r < 16 * q + 16 && r < valid;
+  }
+};
+// Zeroes the rows of the box's groups that PV must not see (each row is 4 slabs x 128 bytes: one
+// 16-byte chunk per lane).
+__device__ __forceinline__ void tc_zero_hidden(uint8_t* box, const TcBox& bx, int lane) {
   uint4* p = reinterpret_cast<uint4*>(box + (lane >> 3) * kTcSlab) + (lane & 7);
-#pragma unroll 8
-  for (int row = v0; row < v1; ++row) p[row * 8] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    if (!bx.group(q)) continue;
+#pragma unroll
+    for (int r = 16 * q; r < 16 * q + 16; ++r)
+      if (!bx.sees(r)) p[r * 8] = make_uint4(0, 0, 0, 0);
+  }
 }
 
-// Rows [h0, h1) of a 64-token box whose first token is `tok0` (in the frame of the map) that are
-// hidden behind the window.
-template <class Map>
-__device__ __forceinline__ void tc_box_hole(const Map& map, int tok0, int& h0, int& h1) {
-  const int r0 = map.real(tok0);
-  h0 = min(max(map.hole0() - r0, 0), 64);
-  h1 = min(max(map.hole1() - r0, 0), 64);
+// The 64-token box whose first token is `tok0` (in the frame of the map) of a segment that ends at t_end.
+template <bool kHoles, class Map>
+__device__ __forceinline__ TcBox tc_box(const Map& map, int tok0, int t_end) {
+  TcBox bx{min(max(t_end - tok0, 0), 64), 0, 0};
+  if (kHoles) {
+    const int r0 = map.real(tok0);
+    bx.h0 = min(max(map.hole0() - r0, 0), 64);
+    bx.h1 = min(max(map.hole1() - r0, 0), 64);
+  }
+  return bx;
 }
 
-// A V box that reaches past the segment end, or (kHoles) holds hidden rows [h0, h1), is loaded through
-// a CTA-local barrier of its slot; once the copy has landed all lanes zero those rows, and the box is
-// published: each lane's proxy fence, the warp barrier, and lane 0's arrival with release semantics on
-// the even CTA's v_full.  Out of line: it runs at most twice per segment (four times with a window).
-// False if the wait failed.
-template <bool kHoles>
-__device__ __noinline__ bool tc_finish_ragged_v(uint8_t* box, uint64_t* fix, uint32_t fix_phase, int rank, int vcount,
-                                                int h0, int h1, uint32_t vfull, volatile int* abort_flag) {
+// A V box with rows that PV must not see is loaded through a CTA-local barrier of its slot; once the
+// copy has landed all lanes zero those rows, and the box is published: each lane's proxy fence, the
+// warp barrier, and lane 0's arrival with release semantics on the even CTA's v_full.  Out of line:
+// it runs at most twice per segment (four times with a window).  False if the wait failed.
+__device__ __noinline__ bool tc_finish_ragged_v(uint8_t* box, uint64_t* fix, uint32_t fix_phase, int rank, TcBox bx,
+                                                uint32_t vfull, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
   int ok = 1;
   if (lane == 0) ok = (mbar_wait(fix, fix_phase, 0x13) && !*abort_flag) ? 1 : 0;
   if (__shfl_sync(0xffffffffu, ok, 0) == 0) return false;
-  if (kHoles) zero_v_rows(box, h0, h1, lane);
-  zero_v_rows(box, vcount, 64, lane);
+  tc_zero_hidden(box, bx, lane);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
@@ -373,21 +394,20 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
       return true;
     };
     auto issue_v = [&](int i) -> bool {
-      int v0[2], vh0[2], vh1[2];   // ragged boxes: valid rows, hidden rows
-      bool ragged[2] = {false, false};
+      TcBox bx[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s, ++vn) {   // box h of a tile sits in slot h
+        const int tok0 = t_begin + i * kTcTile + 64 * s;
+        bx[s] = tc_box<Rows::kHoles>(map, tok0, t_end);
+        const int row = bx[s].valid > 0 ? row_of(tok0) : 0;   // before the wait, which hides the lookup
         if (vn >= kTcVSlots && !wait0(&bars->v_empty[s], static_cast<uint32_t>((vn / kTcVSlots) - 1) & 1u, 0x12))
           return false;
         uint8_t* box = smem + kTcOffV + s * kTcVBox;
-        const int tok0 = t_begin + i * kTcTile + 64 * s;
-        const int vcount = min(max(t_end - tok0, 0), 64);
-        const int row = vcount > 0 ? row_of(tok0) : 0;
         if constexpr (kFp8) {
-          // The converter warps zero the rows past the segment end; a box with none in the
-          // segment is not copied, its barrier completes on the arrival alone.
+          // A box with no token in the segment is not copied, its barrier completes on the arrival
+          // alone.
           if (l0) {
-            if (vcount > 0) {
+            if (bx[s].valid > 0) {
               mbar_arrive_expect_tx(&bars->vraw[s], static_cast<uint32_t>(kTcVBox / 2 + 64));
               tma_load_4d_local(box + kTcFp8OffV, tm_v, &bars->vraw[s], 0, row, 2 * static_cast<int>(rank), 0);
               tma_load_1d(box, tm_sc, &bars->vraw[s], row);
@@ -397,11 +417,9 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
           }
           continue;
         }
-        int h0 = 0, h1 = 0;
-        if (Rows::kHoles) tc_box_hole(map, tok0, h0, h1);
-        if (vcount == 0) {   // no token: PV skips the box, its barrier completes on the arrivals alone
+        if (bx[s].valid == 0) {   // PV skips the box, its barrier completes on the arrivals alone
           if (l0) mbar_arrive_relaxed(lbar(&bars->v_full[s]));
-        } else if (vcount == 64 && h0 == h1) {
+        } else if (bx[s].whole()) {
           if (l0) {
             tma_load_4d_pair(box, tm_v, lbar(&bars->v_full[s]), 0, row, 2 * static_cast<int>(rank), 0);
             if (leader)
@@ -409,25 +427,20 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
             else
               mbar_arrive_relaxed(lbar(&bars->v_full[s]));
           }
-        } else {
-          if (l0) {
-            mbar_arrive_expect_tx(&bars->fix[s], kTcVBox);
-            tma_load_4d_local(box, tm_v, &bars->fix[s], 0, row, 2 * static_cast<int>(rank), 0);
-          }
-          ragged[s] = true;
-          v0[s] = vcount;
-          vh0[s] = h0;
-          vh1[s] = h1;
+        } else if (l0) {
+          mbar_arrive_expect_tx(&bars->fix[s], kTcVBox);
+          tma_load_4d_local(box, tm_v, &bars->fix[s], 0, row, 2 * static_cast<int>(rank), 0);
         }
       }
+      if constexpr (!kFp8) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {   // with both copies on their way
-        if (!ragged[s]) continue;
-        if (!tc_finish_ragged_v<Rows::kHoles>(smem + kTcOffV + s * kTcVBox, &bars->fix[s], (fix_phase >> s) & 1u,
-                                              static_cast<int>(rank), v0[s], vh0[s], vh1[s],
-                                              lbar(&bars->v_full[s]), abort_flag))
-          return false;
-        fix_phase ^= 1u << s;
+        for (int s = 0; s < 2; ++s) {   // with both copies on their way
+          if (bx[s].valid == 0 || bx[s].whole()) continue;
+          if (!tc_finish_ragged_v(smem + kTcOffV + s * kTcVBox, &bars->fix[s], (fix_phase >> s) & 1u,
+                                  static_cast<int>(rank), bx[s], lbar(&bars->v_full[s]), abort_flag))
+            return false;
+          fix_phase ^= 1u << s;
+        }
       }
       return true;
     };
@@ -514,6 +527,8 @@ __device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, int nh, co
       ok = false;
       break;
     }
+    const auto map = rows.map(sg.len);
+    uint32_t acc = 0;   // the segment's first MMA overwrites O
     for (int i = 0; i < sg.n_tiles && ok; ++i, ++g) {
       if (!mbar_wait_cluster(&bars->p_full, static_cast<uint32_t>(g) & 1u, 0x22)) {
         ok = false;
@@ -530,11 +545,18 @@ __device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, int nh, co
         tc_fence_after();
         const uint64_t pb = sdesc_add(dp, h * kTcSlab);
         const uint64_t vb = sdesc_add(dv, vs * kTcVBox);
-        if (h == 0 || sg.tok_begin + i * kTcTile + 64 < sg.tok_end) {
+        const TcBox bx = tc_box<Rows::kHoles>(map, sg.tok_begin + i * kTcTile + 64 * h, sg.tok_end);
+        if (bx.whole()) {
 #pragma unroll
-        for (int g4 = 0; g4 < 4; ++g4)   // 16-token groups; the segment's first MMA overwrites O
-          umma_bf16_pair(ocol, sdesc_add(pb, 32 * g4), sdesc_add(vb, g4 * 2048), idesc_pv,
-                         (i > 0 || h > 0 || g4 > 0) ? 1u : 0u);
+          for (int g4 = 0; g4 < 4; ++g4, acc = 1)   // 16-token groups
+            umma_bf16_pair(ocol, sdesc_add(pb, 32 * g4), sdesc_add(vb, g4 * 2048), idesc_pv, acc);
+        } else {
+#pragma unroll 1
+          for (int g4 = 0; g4 < 4; ++g4) {
+            if (!bx.group(g4)) continue;
+            umma_bf16_pair(ocol, sdesc_add(pb, 32 * g4), sdesc_add(vb, g4 * 2048), idesc_pv, acc);
+            acc = 1;
+          }
         }
         umma_commit_pair_mc(&bars->v_empty[vs], 3);
       }
@@ -579,12 +601,12 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& c, float mult, uint
 // One box: wait for its codes and scale bytes (a CTA-local barrier), read this thread's chunks and
 // its two rows' scales, meet the other converter threads (the buffer is then free to overwrite),
 // write the bf16 values into the 128-byte-swizzled slab layout of the buffer (rows at or past
-// `vcount` as zeros), and publish the buffer on the even CTA's barrier `done`.  The staged codes
+// `bx.valid`, and hidden ones, as zeros), and publish the buffer on the even CTA's barrier `done`.  The staged codes
 // are laid out [slab][row][64 bytes], so converter thread ct takes chunk ct + 128 j: piece ct & 3
 // of row (ct >> 2) + 32 (j & 1) of slab j >> 1.  False (the same in every converter thread) if
 // the wait failed or the kernel is aborting.
 template <int kSlabs, bool kHoles>
-__device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, int vcount, int h0, int h1, uint64_t* raw,
+__device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, const TcBox& bx, uint64_t* raw,
                                                uint32_t parity, uint32_t done, volatile int* abort_flag, int ct) {
   const bool got = mbar_wait(raw, parity, 0x17) && !*abort_flag;
   if (!named_bar_red_and(3, kTcConvThreads, got)) return false;
@@ -601,7 +623,7 @@ __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, int 
   for (int j = 0; j < 2 * kSlabs; ++j) {
     const int row = rb + 32 * (j & 1);
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (row < vcount && !(kHoles && row >= h0 && row < h1)) e4m3x16_to_bf16(c[j], (j & 1) ? m1 : m0, lo, hi);
+    if (row < bx.valid && !(kHoles && row >= bx.h0 && row < bx.h1)) e4m3x16_to_bf16(c[j], (j & 1) ? m1 : m0, lo, hi);
     uint8_t* dst = buf + (j >> 1) * kTcSlab + row * 128;
     *reinterpret_cast<uint4*>(dst + (((2 * pc) ^ (row & 7)) << 4)) = lo;
     *reinterpret_cast<uint4*>(dst + (((2 * pc + 1) ^ (row & 7)) << 4)) = hi;
@@ -626,24 +648,22 @@ __device__ bool tc_convert(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   int g = 0, vn = 0;
   bool ok = true;
   const Rows rows = tc_rows<Rows>(a);
+  const TcBox kAll{64, 0, 0};
   while (ok && cur.next(a.seq_lens, a.capacity, rows, sg)) {
     const auto map = rows.map(sg.len);
     const int t_begin = sg.tok_begin, t_end = sg.tok_end, n_tiles = sg.n_tiles;
     for (int i = 0; ok && i <= n_tiles; ++i) {
       if (i < n_tiles) {
         const uint32_t par = static_cast<uint32_t>(g + i) & 1u;
-        ok = tc_convert_box<kTcKSlabsA, false>(smem + kTcOffK, kTcFp8OffA, 64, 0, 0, &bars->kraw[0], par,
+        ok = tc_convert_box<kTcKSlabsA, false>(smem + kTcOffK, kTcFp8OffA, kAll, &bars->kraw[0], par,
                                                lbar(&bars->k_full[0]), abort_flag, ct) &&
-             tc_convert_box<kTcKSlabsB, false>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, 64, 0, 0,
+             tc_convert_box<kTcKSlabsB, false>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, kAll,
                                                &bars->kraw[1], par, lbar(&bars->k_full[1]), abort_flag, ct);
       }
       for (int h = 0; ok && i > 0 && h < 2; ++h, ++vn) {
         const int s = vn % kTcVSlots;
-        const int tok0 = t_begin + (i - 1) * kTcTile + 64 * h;
-        const int vcount = min(max(t_end - tok0, 0), 64);
-        int h0 = 0, h1 = 0;
-        if (Rows::kHoles) tc_box_hole(map, tok0, h0, h1);
-        ok = tc_convert_box<4, Rows::kHoles>(smem + kTcOffV + s * kTcVBox, kTcFp8OffV, vcount, h0, h1, &bars->vraw[s],
+        const TcBox bx = tc_box<Rows::kHoles>(map, t_begin + (i - 1) * kTcTile + 64 * h, t_end);
+        ok = tc_convert_box<4, Rows::kHoles>(smem + kTcOffV + s * kTcVBox, kTcFp8OffV, bx, &bars->vraw[s],
                                              static_cast<uint32_t>(vn / kTcVSlots) & 1u, lbar(&bars->v_full[s]),
                                              abort_flag, ct);
       }
