@@ -82,24 +82,20 @@ constexpr int kTcOffBar = kTcOffV + kTcVSlots * kTcVBox;
 constexpr int kTcOffMisc = kTcOffBar + 256;
 constexpr int kTcSmemBytes = kTcOffMisc + 64 + 2 * 256 * 4;   // the dynamic base is 1024-aligned (checked)
 
-// TMEM columns of each CTA (512 allocated): S of QK^T issuer 0 (2 buffers x 64), of issuer 1
-// (2 x 64), O (256).
-constexpr uint32_t kTcColSA = 0;
-constexpr uint32_t kTcColSB = 128;
+// TMEM columns of each CTA (512 allocated): S (2 buffers x 64), O (256).
+constexpr uint32_t kTcColS = 0;
 constexpr uint32_t kTcColO = 256;
 
 constexpr int kTcSoftmaxWarps = 8;
-constexpr int kTcProducerWarp = 8;
-constexpr int kTcMmaWarp = 9;     // TMEM allocation (both CTAs); QK^T even K steps (even CTA)
-constexpr int kTcPvWarp = 10;     // PV issue, first latent half (even CTA)
-constexpr int kTcMmaBWarp = 11;   // QK^T odd K steps (even CTA)
-constexpr int kTcPv1Warp = 12;    // PV issue, second latent half (even CTA)
-constexpr int kTcVProducerWarp = 13;
-constexpr int kTcThreads = 32 * (kTcSoftmaxWarps + 6);
-// FP8 cache: four converter warps after the others.
-constexpr int kTcConvWarp0 = kTcSoftmaxWarps + 6;
+constexpr int kTcProducerWarp = 8;    // work plan, then Q and K copies
+constexpr int kTcMmaWarp = 9;         // TMEM allocation (both CTAs); QK^T issue (even CTA)
+constexpr int kTcPvWarp = 10;         // PV issue (even CTA)
+constexpr int kTcVProducerWarp = 11;  // V copies
+constexpr int kTcThreads = 32 * (kTcSoftmaxWarps + 4);
+// FP8 cache: four converter warps for K and four for V after the others.
+constexpr int kTcConvWarp0 = kTcSoftmaxWarps + 4;
 constexpr int kTcConvThreads = 128;
-constexpr int kTcThreadsFp8 = kTcThreads + kTcConvThreads;
+constexpr int kTcThreadsFp8 = kTcThreads + 2 * kTcConvThreads;
 __host__ __device__ constexpr int tc_threads(bool fp8) { return fp8 ? kTcThreadsFp8 : kTcThreads; }
 // Where the codes of a box wait for conversion: the upper half of the bf16 buffer they become.
 constexpr int kTcFp8OffA = kTcKSlabsA * kTcSlab / 2;
@@ -139,19 +135,19 @@ struct TcPlan {
 
 struct TcBars {
   uint64_t k_full[2];            // even CTA only, per QK^T part: both CTAs' K boxes landed (one arrival per CTA + tx)
-  uint64_t k_empty[2];           // both CTAs, per part: K box consumed by the MMAs (one commit per QK^T issuer)
+  uint64_t k_empty[2];           // both CTAs, per part: K box consumed by the MMAs
   uint64_t v_full[kTcVSlots];    // even CTA only: both CTAs' V box landed (one arrival per CTA + tx)
-  uint64_t v_empty[kTcVSlots];   // both CTAs: V box consumed (one commit per PV warp)
+  uint64_t v_empty[kTcVSlots];   // both CTAs: V box consumed
   uint64_t fix[kTcVSlots];       // per CTA and slot: local load of a ragged V box
-  uint64_t s_full[2];            // both: QK^T of a tile done (one commit per part)
+  uint64_t s_full[2];            // both: QK^T of a tile done
   uint64_t s_empty[2];           // even CTA only: every softmax warp of both CTAs has read S
-  uint64_t p_full;               // even CTA only: P (and corrected O) of a tile ready in both CTAs
-  uint64_t p_empty;              // both: PV of a tile done reading P (one commit per PV warp)
-  uint64_t o_ready;              // both: PV of a tile done writing O (one phase per tile, two commits)
-  uint64_t o_final;              // both: the last PV of a segment done (one phase per segment, two commits)
+  uint64_t p_full[2];            // even CTA only, per 64-token half: P ready in both CTAs (half 0: O corrected too)
+  uint64_t p_empty[2];           // both, per half: PV of a tile done reading P
+  uint64_t o_ready;              // both: PV of a tile done writing O (one phase per tile)
+  uint64_t o_final;              // both: the last PV of a segment done (one phase per segment)
   uint64_t o_free;               // both: every softmax warp of both CTAs has read O of a segment
   uint64_t q_full;               // even CTA only: Q of both CTAs landed (one phase per segment)
-  uint64_t q_empty;              // both: QK^T of a segment's last tile done (two commits)
+  uint64_t q_empty;              // both: QK^T of a segment's last tile done
   uint64_t kraw[2];              // FP8, per CTA and part: this CTA's K codes and scales landed (+ tx)
   uint64_t vraw[kTcVSlots];      // FP8, per CTA and slot: this CTA's V codes and scales landed (+ tx)
 };
@@ -452,35 +448,29 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
 }
 
 // ------------------------------------------------------------------------------ MMA issuers (even CTA)
-// A single issuing thread cannot keep the tensor pipe busy with these shapes (each tcgen05.mma
-// holds its thread for about as long as the pair takes to execute an M = 128, N = 128, K = 16
-// step), so four warps issue: QK^T part A, QK^T part B (separate S accumulators over disjoint
-// dims) and PV (two warps, one per latent half).  QK^T of tile i + 1 then runs on the tensor cores while the softmax warps work on
-// tile i and PV of tile i - 1 completes.
+// One elected thread issues QK^T and one PV.  Both shapes then run at the tensor pipe's full rate (M = 128
+// pair, cycles per K step of 16: N = 128 32.6, N = 256 64.6; from a thread chosen by its lane number 52.9 and
+// 64.6): QK^T of tile i + 1 shares the pipe with PV of tile i, and the softmax warps work in between.
 
 // Advance a shared-memory descriptor by `bytes` (a multiple of 16): the start address field
 // holds address / 16 in its low 14 bits, and every operand here lies below 256 KB, so the sum
 // never carries out of the field.
 __device__ __forceinline__ uint64_t sdesc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
-// S_j(g) = the sum over the 16-deep K steps (slab c, step kk) with kk % 2 == j of Q . K(g)^T, into
-// S buffer g & 1 of issuer j (the softmax adds S_0 + S_1), for every global tile g of the range; Q
-// is reloaded for each segment.  Both issuers walk the part-A slabs (0-4) first and then part B's
-// (5-8), so part A's K slot is released halfway through the tile's QK^T (its next copy then
-// overlaps the second half and PV) and QK^T of the next tile needs part B's copy only halfway in.
+// S(g) = Q . K(g)^T into S buffer g & 1, for every global tile g of the range; Q is reloaded for each
+// segment.  Part A's slabs come first, so its K slot is released halfway through the tile's QK^T.
 template <class Rows>
-__device__ bool tc_mma_qk(uint8_t* smem, TcBars* bars, uint32_t tmem, int j, const int32_t* seq_lens, int capacity,
+__device__ bool tc_mma_qk(uint8_t* smem, TcBars* bars, uint32_t tmem, const int32_t* seq_lens, int capacity,
                           const Rows rows, SegmentCursor cur, volatile int* abort_flag) {
   const uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
   const uint64_t dq = sdesc_sw128(smem_u32(smem + kTcOffQ), 16, 1024);
   const uint64_t dk = sdesc_sw128(smem_u32(smem + kTcOffK), 16, 1024);
-  const uint32_t scol = tmem + (j ? kTcColSB : kTcColSA);
   Segment sg;
   int g = 0, k = 0;
   while (cur.next(seq_lens, capacity, rows, sg)) {
     if (!mbar_wait_cluster(&bars->q_full, static_cast<uint32_t>(k) & 1u, 0x20)) return false;
     for (int i = 0; i < sg.n_tiles; ++i, ++g) {
-      const uint32_t sb = scol + 64 * (g & 1);
+      const uint32_t sb = tmem + kTcColS + 64 * (g & 1);
       // S buffer g & 1 last held tile g - 2: every softmax warp of both CTAs must have read it.
       if (g >= 2 && !mbar_wait_cluster(&bars->s_empty[g & 1], static_cast<uint32_t>((g - 2) >> 1) & 1u, 0x24))
         return false;
@@ -488,13 +478,12 @@ __device__ bool tc_mma_qk(uint8_t* smem, TcBars* bars, uint32_t tmem, int j, con
       for (int part = 0; part < 2; ++part) {
         if (!mbar_wait_cluster(&bars->k_full[part], static_cast<uint32_t>(g) & 1u, 0x21)) return false;
         tc_fence_after();
-        // Fully unrolled (the issue rate of this thread bounds the tensor pipe here): every
-        // descriptor is a constant offset from the base.
+        // Fully unrolled: every descriptor is a constant offset from the base.
 #pragma unroll
         for (int c = tc_part_slab0(part); c < tc_part_slab0(part) + tc_part_slabs(part); ++c)
 #pragma unroll
-          for (int kk = 0; kk < 4; kk += 2) {
-            const uint32_t off = c * kTcSlab + 32 * (kk + j);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t off = c * kTcSlab + 32 * kk;
             umma_bf16_pair(sb, sdesc_add(dq, off), sdesc_add(dk, off), idesc_qk, (c | kk) != 0 ? 1u : 0u);
           }
         umma_commit_pair_mc(&bars->k_empty[part], 3);
@@ -508,17 +497,16 @@ __device__ bool tc_mma_qk(uint8_t* smem, TcBars* bars, uint32_t tmem, int j, con
   return true;
 }
 
-// O[:, latent half nh] += P(g) . V(g)[:, half nh].  Two warps issue, one per half (separate
-// accumulators); every release below therefore counts two commits.  The first V box (tokens
-// 0..63 of the tile) is consumed first so it is released (and refilled) before the second.  The
-// first tile of a segment overwrites O, after the previous segment's epilogue has read it.
+// O[:, latent half n] += P(g) . V(g)[:, half n] for both halves.  The first 64-token half of the tile is
+// consumed first, as soon as its P is ready, and its P and V box are released before the second's.
+// The first tile of a segment overwrites O, after the previous segment's epilogue has read it.
 template <class Rows>
-__device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, int nh, const int32_t* seq_lens,
-                          int capacity, const Rows rows, SegmentCursor cur, volatile int* abort_flag) {
+__device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, const int32_t* seq_lens, int capacity,
+                          const Rows rows, SegmentCursor cur, volatile int* abort_flag) {
   const uint32_t idesc_pv = idesc_bf16_f32(128, 256, false, true);
   const uint64_t dp = sdesc_sw128(smem_u32(smem + kTcOffP), 16, 1024);
-  const uint64_t dv = sdesc_sw128(smem_u32(smem + kTcOffV + nh * 2 * kTcSlab), kTcSlab, 1024);
-  const uint32_t ocol = tmem + kTcColO + 128 * nh;
+  const uint64_t dv = sdesc_sw128(smem_u32(smem + kTcOffV), kTcSlab, 1024);
+  const uint32_t ocol = tmem + kTcColO;
   Segment sg;
   int g = 0, k = 0;
   bool ok = true;
@@ -530,38 +518,37 @@ __device__ bool tc_mma_pv(uint8_t* smem, TcBars* bars, uint32_t tmem, int nh, co
     const auto map = rows.map(sg.len);
     uint32_t acc = 0;   // the segment's first MMA overwrites O
     for (int i = 0; i < sg.n_tiles && ok; ++i, ++g) {
-      if (!mbar_wait_cluster(&bars->p_full, static_cast<uint32_t>(g) & 1u, 0x22)) {
-        ok = false;
-        break;
-      }
       // V box 2g + h sits in slot h of the 2-slot ring, in its (g + 1)-th fill.
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int vs = h;
-        if (!mbar_wait_cluster(&bars->v_full[vs], static_cast<uint32_t>(g) & 1u, 0x23)) {
+        if (!mbar_wait_cluster(&bars->p_full[h], static_cast<uint32_t>(g) & 1u, 0x22) ||
+            !mbar_wait_cluster(&bars->v_full[h], static_cast<uint32_t>(g) & 1u, 0x23)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint64_t pb = sdesc_add(dp, h * kTcSlab);
-        const uint64_t vb = sdesc_add(dv, vs * kTcVBox);
+        const uint64_t vb = sdesc_add(dv, h * kTcVBox);
         const TcBox bx = tc_box<Rows::kHoles>(map, sg.tok_begin + i * kTcTile + 64 * h, sg.tok_end);
+        auto group = [&](int g4) {   // 16 tokens, both latent halves
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            umma_bf16_pair(ocol + 128 * n, sdesc_add(pb, 32 * g4), sdesc_add(vb, n * 2 * kTcSlab + g4 * 2048), idesc_pv,
+                           acc);
+          acc = 1;
+        };
         if (bx.whole()) {
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4, acc = 1)   // 16-token groups
-            umma_bf16_pair(ocol, sdesc_add(pb, 32 * g4), sdesc_add(vb, g4 * 2048), idesc_pv, acc);
+          for (int g4 = 0; g4 < 4; ++g4) group(g4);
         } else {
 #pragma unroll 1
-          for (int g4 = 0; g4 < 4; ++g4) {
-            if (!bx.group(g4)) continue;
-            umma_bf16_pair(ocol, sdesc_add(pb, 32 * g4), sdesc_add(vb, g4 * 2048), idesc_pv, acc);
-            acc = 1;
-          }
+          for (int g4 = 0; g4 < 4; ++g4)
+            if (bx.group(g4)) group(g4);
         }
-        umma_commit_pair_mc(&bars->v_empty[vs], 3);
+        umma_commit_pair_mc(&bars->v_empty[h], 3);
+        umma_commit_pair_mc(&bars->p_empty[h], 3);
       }
       if (!ok) break;
-      umma_commit_pair_mc(&bars->p_empty, 3);
       umma_commit_pair_mc(&bars->o_ready, 3);
       if (*abort_flag) ok = false;
     }
@@ -607,9 +594,10 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& c, float mult, uint
 // the wait failed or the kernel is aborting.
 template <int kSlabs, bool kHoles>
 __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, const TcBox& bx, uint64_t* raw,
-                                               uint32_t parity, uint32_t done, volatile int* abort_flag, int ct) {
+                                               uint32_t parity, uint32_t done, volatile int* abort_flag, int ct,
+                                               int bar_id) {
   const bool got = mbar_wait(raw, parity, 0x17) && !*abort_flag;
-  if (!named_bar_red_and(3, kTcConvThreads, got)) return false;
+  if (!named_bar_red_and(bar_id, kTcConvThreads, got)) return false;
   const int pc = ct & 3;
   const int rb = ct >> 2;
   uint4 c[2 * kSlabs];
@@ -618,7 +606,7 @@ __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, cons
     c[j] = *reinterpret_cast<const uint4*>(buf + codes_off + 16 * (ct + kTcConvThreads * j));
   const float m0 = e8m0_value(buf[rb]);
   const float m1 = e8m0_value(buf[rb + 32]);
-  named_bar_sync(3, kTcConvThreads);   // every staged byte has been read
+  named_bar_sync(bar_id, kTcConvThreads);   // every staged byte has been read
 #pragma unroll
   for (int j = 0; j < 2 * kSlabs; ++j) {
     const int row = rb + 32 * (j & 1);
@@ -629,7 +617,7 @@ __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, cons
     *reinterpret_cast<uint4*>(dst + (((2 * pc + 1) ^ (row & 7)) << 4)) = hi;
   }
   fence_proxy_async_smem();
-  named_bar_sync(3, kTcConvThreads);
+  named_bar_sync(bar_id, kTcConvThreads);
   if (ct == 0) {
     fence_release_smem_to_cluster();
     mbar_arrive_relaxed(done);
@@ -637,38 +625,36 @@ __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, cons
   return true;
 }
 
-// The converter warps walk the boxes in the producer's order: K(0), K(1), V(0), K(2), V(1), ...
-// (both parts of a K tile, then both 64-token V boxes of a tile).
+// Four converter warps walk the K boxes (both parts of each tile), four the V boxes (both 64-token
+// halves of each tile).
 template <class Rows>
 __device__ bool tc_convert(const DecodeTcArgs& a, const TcPlan& plan, int pair, uint8_t* smem, TcBars* bars,
                            volatile int* abort_flag) {
-  const int ct = static_cast<int>(threadIdx.x) - 32 * kTcConvWarp0;
+  const int grp = static_cast<int>(threadIdx.x) / 32 >= kTcConvWarp0 + 4;
+  const int ct = static_cast<int>(threadIdx.x) - 32 * kTcConvWarp0 - grp * kTcConvThreads;
   SegmentCursor cur{plan.b0, plan.off0, plan.start, plan.end, plan.b_end, pair, true, plan.len0};
   Segment sg;
-  int g = 0, vn = 0;
+  uint32_t g = 0;
   bool ok = true;
   const Rows rows = tc_rows<Rows>(a);
-  const TcBox kAll{64, 0, 0};
   while (ok && cur.next(a.seq_lens, a.capacity, rows, sg)) {
     const auto map = rows.map(sg.len);
-    const int t_begin = sg.tok_begin, t_end = sg.tok_end, n_tiles = sg.n_tiles;
-    for (int i = 0; ok && i <= n_tiles; ++i) {
-      if (i < n_tiles) {
-        const uint32_t par = static_cast<uint32_t>(g + i) & 1u;
-        ok = tc_convert_box<kTcKSlabsA, false>(smem + kTcOffK, kTcFp8OffA, kAll, &bars->kraw[0], par,
-                                               lbar(&bars->k_full[0]), abort_flag, ct) &&
-             tc_convert_box<kTcKSlabsB, false>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, kAll,
-                                               &bars->kraw[1], par, lbar(&bars->k_full[1]), abort_flag, ct);
-      }
-      for (int h = 0; ok && i > 0 && h < 2; ++h, ++vn) {
-        const int s = vn % kTcVSlots;
-        const TcBox bx = tc_box<Rows::kHoles>(map, t_begin + (i - 1) * kTcTile + 64 * h, t_end);
-        ok = tc_convert_box<4, Rows::kHoles>(smem + kTcOffV + s * kTcVBox, kTcFp8OffV, bx, &bars->vraw[s],
-                                             static_cast<uint32_t>(vn / kTcVSlots) & 1u, lbar(&bars->v_full[s]),
-                                             abort_flag, ct);
+    for (int i = 0; ok && i < sg.n_tiles; ++i, ++g) {
+      const uint32_t par = g & 1u;
+      if (grp == 0) {
+        const TcBox all{64, 0, 0};
+        ok = tc_convert_box<kTcKSlabsA, false>(smem + kTcOffK, kTcFp8OffA, all, &bars->kraw[0], par,
+                                               lbar(&bars->k_full[0]), abort_flag, ct, 3) &&
+             tc_convert_box<kTcKSlabsB, false>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, all, &bars->kraw[1],
+                                               par, lbar(&bars->k_full[1]), abort_flag, ct, 3);
+      } else {
+        for (int h = 0; ok && h < 2; ++h) {
+          const TcBox bx = tc_box<Rows::kHoles>(map, sg.tok_begin + i * kTcTile + 64 * h, sg.tok_end);
+          ok = tc_convert_box<4, Rows::kHoles>(smem + kTcOffV + h * kTcVBox, kTcFp8OffV, bx, &bars->vraw[h], par,
+                                               lbar(&bars->v_full[h]), abort_flag, ct, 4);
+        }
       }
     }
-    g += n_tiles;
   }
   return ok;
 }
@@ -869,16 +855,14 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       break;
     }
     tc_fence_after();
-    // S = S_0 + S_1 (the two QK^T issuers' sums over disjoint K steps).
     float sc[32];
+    {
+      uint32_t ra[2][16];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t ra[16], rb[16];
-      tmem_ld16(tmem + lane_base + kTcColSA + 64 * j + 32 * ch + 16 * q, ra);
-      tmem_ld16(tmem + lane_base + kTcColSB + 64 * j + 32 * ch + 16 * q, rb);
+      for (int q = 0; q < 2; ++q) tmem_ld16(tmem + lane_base + kTcColS + 64 * j + 32 * ch + 16 * q, ra[q]);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sc[16 * q + e] = __uint_as_float(ra[e]) + __uint_as_float(rb[e]);
+      for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(ra[e >> 4][e & 15]);
     }
     // S is in registers (tcgen05.wait::ld above): its TMEM buffer may take tile i + 2.  The
     // arrival orders nothing else, so it is relaxed.
@@ -944,10 +928,12 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
       pk[e] = *reinterpret_cast<uint32_t*>(&h2);
     }
-    // The P buffer is free once PV(g-1) has read it.  By parity this is unambiguous for the
-    // same reason: p_empty has completed g-1 or g phases.  Between segments the epilogue waits for
-    // more (all of PV), reads O and stages it through the P buffer; the barrier then lets every
-    // warp write P, and both CTAs learn that O may be overwritten.
+    // A half of the P buffer is free once PV(g-1) has read it.  By parity this is unambiguous for the
+    // same reason: p_empty has completed g-1 or g phases.  PV of the first half needs O corrected by
+    // every warp, so the second half's warps arrive for it too, without waiting for their own half
+    // (but for the first one's: no arrival for tile g before PV(g-1) has taken all of tile g-1).
+    // Between segments the epilogue waits for more (all of PV), reads O and stages it through the
+    // P buffer; the barrier then lets every warp write P, and both CTAs learn that O may be overwritten.
     if (i == 0 && k > 0) {
       epilogue(k - 1, red + (j ^ 1) * 256);
       tc_fence_before();
@@ -958,9 +944,18 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
         mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 0));
         mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 1));
       }
-    } else if (g >= 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->p_empty, static_cast<uint32_t>(g - 1) & 1u, 0x32))) {
+    } else if (g >= 1 &&
+               !__all_sync(0xffffffffu, mbar_wait(&bars->p_empty[0], static_cast<uint32_t>(g - 1) & 1u, 0x32))) {
       ok = false;
       break;
+    }
+    if (half == 1) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(lbar(&bars->p_full[0]));
+      // (only these warps wait here: a failure is left to the waits that all of them share)
+      if (g >= 1 && !mbar_wait(&bars->p_empty[1], static_cast<uint32_t>(g - 1) & 1u, 0x34)) *abort_flag = 1;
+      __syncwarp();
     }
     uint8_t* prow = smem + kTcOffP + half * kTcSlab + hl * 128;
 #pragma unroll
@@ -979,7 +974,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     __syncwarp();
     if (lane == 0) {
       fence_release_smem_to_cluster();
-      mbar_arrive_relaxed(lbar(&bars->p_full));
+      mbar_arrive_relaxed(lbar(&bars->p_full[half]));
     }
     if (i + kTcPfDist < n_tiles)
       tc_prefetch_tile<kMapped>(a, map, sg.b, t_begin + (i + kTcPfDist) * kTcTile + 64 * static_cast<int>(rank), t_end);
@@ -1198,24 +1193,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
   if (threadIdx.x == 0) {
     for (int part = 0; part < 2; ++part) {
       mbar_init(&bars->k_full[part], 2);   // one arrival per CTA of the pair (plus the copies' bytes)
-      mbar_init(&bars->k_empty[part], 2);   // one commit per QK^T issuer
+      mbar_init(&bars->k_empty[part], 1);
     }
     for (int s = 0; s < kTcVSlots; ++s) {
       mbar_init(&bars->v_full[s], 2);   // one arrival per CTA of the pair (plus the copies' bytes)
-      mbar_init(&bars->v_empty[s], 2);   // one commit per PV warp
+      mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->fix[s], 1);
     }
-    mbar_init(&bars->s_full[0], 2);   // one commit per QK^T part
-    mbar_init(&bars->s_full[1], 2);
+    mbar_init(&bars->s_full[0], 1);
+    mbar_init(&bars->s_full[1], 1);
     mbar_init(&bars->s_empty[0], 2 * kTcSoftmaxWarps);   // every softmax warp of both CTAs
     mbar_init(&bars->s_empty[1], 2 * kTcSoftmaxWarps);
-    mbar_init(&bars->p_full, 2 * kTcSoftmaxWarps);   // every softmax warp of both CTAs
-    mbar_init(&bars->p_empty, 2);   // one commit per PV warp
-    mbar_init(&bars->o_ready, 2);
-    mbar_init(&bars->o_final, 2);
+    mbar_init(&bars->p_full[0], 2 * kTcSoftmaxWarps);   // every softmax warp of both CTAs
+    mbar_init(&bars->p_full[1], kTcSoftmaxWarps);       // those of the second token half
+    mbar_init(&bars->p_empty[0], 1);
+    mbar_init(&bars->p_empty[1], 1);
+    mbar_init(&bars->o_ready, 1);
+    mbar_init(&bars->o_final, 1);
     mbar_init(&bars->o_free, 2 * kTcSoftmaxWarps);   // every softmax warp of both CTAs
     mbar_init(&bars->q_full, 2);
-    mbar_init(&bars->q_empty, 2);   // one commit per QK^T part
+    mbar_init(&bars->q_empty, 1);
     if (kFp8) {
       for (int part = 0; part < 2; ++part) mbar_init(&bars->kraw[part], 1);   // this CTA's producer (plus bytes)
       for (int s = 0; s < kTcVSlots; ++s) mbar_init(&bars->vraw[s], 1);
@@ -1268,16 +1265,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
                                                                  bars, rank, pair, abort_flag);
     if (!ok && (threadIdx.x & 31) == 0) *abort_flag = 1;
   } else if (kFp8 && warp >= kTcConvWarp0) {
-    if (!tc_convert<Rows>(a, pl, pair, smem, bars, abort_flag) && threadIdx.x == 32 * kTcConvWarp0)
-      *abort_flag = 1;
+    if (!tc_convert<Rows>(a, pl, pair, smem, bars, abort_flag) && (threadIdx.x & 127) == 0) *abort_flag = 1;
   } else if (rank == 0 && elect_one()) {
-    bool ok = true;
-    // One out-of-line copy of each issuer serves both of its warps (part / latent half as argument).
     const SegmentCursor cur{pl.b0, pl.off0, pl.start, pl.end, pl.b_end, pair, true, pl.len0};
-    if (warp == kTcMmaWarp || warp == kTcMmaBWarp)
-      ok = tc_mma_qk(smem, bars, tmem, warp == kTcMmaWarp ? 0 : 1, a.seq_lens, a.capacity, tc_rows<Rows>(a), cur, abort_flag);
-    else
-      ok = tc_mma_pv(smem, bars, tmem, warp == kTcPvWarp ? 0 : 1, a.seq_lens, a.capacity, tc_rows<Rows>(a), cur, abort_flag);
+    const bool ok = warp == kTcMmaWarp
+                        ? tc_mma_qk(smem, bars, tmem, a.seq_lens, a.capacity, tc_rows<Rows>(a), cur, abort_flag)
+                        : tc_mma_pv(smem, bars, tmem, a.seq_lens, a.capacity, tc_rows<Rows>(a), cur, abort_flag);
     if (!ok) *abort_flag = 1;
   }
   __syncwarp();
