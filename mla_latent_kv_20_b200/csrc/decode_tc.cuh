@@ -175,42 +175,6 @@ __device__ __forceinline__ int tc_cache_seq(const DecodeTcArgs& a, int b, bool r
   return -1;
 }
 
-// Block ids of a paged cache for the producer warp, so that the row of a copy needs no dependent
-// load of the block table on the way to the copy (211 instead of 223 us for the batch-128 paged
-// workload, A/B on identical inputs): lane l holds the ids of pages wp + l (cur) and wp + 32 + l
-// (nxt) of cache sequence b.  A lookup past wp + 48 slides the window by 32 pages and requests the
-// next 32 ids then, 16 pages (8 tiles) before they are needed; lookups stay within 16 pages behind
-// the furthest one (the V copies of a tile follow the K copy of the next one).
-struct PageWindow {
-  int b = -1, wp = 0, cur = -1, nxt = -1;
-};
-__device__ __forceinline__ int pw_entry(const CacheView& v, int b, int p) {
-  return (p >= 0 && p < v.max_blocks) ? v.block_table[static_cast<int64_t>(b) * v.max_blocks + p] : -1;
-}
-// TMA row of token t of cache sequence b (every lane calls it with the same arguments and gets the
-// same row), or -kTcTile (a fully out-of-bounds box) with the error word set for a bad block id.
-__device__ __forceinline__ int pw_row(PageWindow& w, const CacheView& v, int b, int t, int lane) {
-  const int p = t / kPage;
-  if (b != w.b || p < w.wp || p >= w.wp + 64) {
-    w.b = b;
-    w.wp = p & ~31;
-    w.cur = pw_entry(v, b, w.wp + lane);
-    w.nxt = pw_entry(v, b, w.wp + 32 + lane);
-  } else if (p >= w.wp + 48) {
-    w.cur = w.nxt;
-    w.wp += 32;
-    w.nxt = pw_entry(v, b, w.wp + 32 + lane);
-  }
-  const int d = p - w.wp;
-  const int blk = __shfl_sync(0xffffffffu, d < 32 ? w.cur : w.nxt, d & 31);
-  const int64_t r = static_cast<int64_t>(blk) * kPage + (t % kPage);
-  if (blk < 0 || r >= v.num_rows) {
-    if (lane == 0) set_dev_error(0x2);
-    return -kTcTile;
-  }
-  return static_cast<int>(r);
-}
-
 // 3-D TMA load (x: element in a 64-wide dim-slab, y: cache row, z: dim-slab) into this CTA's
 // shared memory; completion counted on a barrier that may live in the peer CTA.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar_cluster_addr, int x,
@@ -266,15 +230,19 @@ struct TcBox {
   }
 };
 // Zeroes the rows of the box's groups that PV must not see (each row is 4 slabs x 128 bytes: one
-// 16-byte chunk per lane).
+// 16-byte chunk per lane): behind the valid ones, and at both ends of the hidden run, to the border
+// of the group.  Short loops: this code is cold whenever it runs, and its fetches cost more than its work.
 __device__ __forceinline__ void tc_zero_hidden(uint8_t* box, const TcBox& bx, int lane) {
   uint4* p = reinterpret_cast<uint4*>(box + (lane >> 3) * kTcSlab) + (lane & 7);
 #pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    if (!bx.group(q)) continue;
-#pragma unroll
-    for (int r = 16 * q; r < 16 * q + 16; ++r)
-      if (!bx.sees(r)) p[r * 8] = make_uint4(0, 0, 0, 0);
+  for (int u = 0; u < 3; ++u) {
+    int r = bx.valid, end = (bx.valid + 15) & ~15;
+    if (u > 0) {
+      r = u == 1 ? bx.h0 : max(bx.h0, bx.h1 & ~15);
+      end = u == 1 ? min(bx.h1, (bx.h0 + 15) & ~15) : bx.h1;
+    }
+#pragma unroll 1
+    for (; r < end; ++r) p[r * 8] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -292,9 +260,9 @@ __device__ __forceinline__ TcBox tc_box(const Map& map, int tok0, int t_end) {
 
 // A V box with rows that PV must not see is loaded through a CTA-local barrier of its slot; once the
 // copy has landed all lanes zero those rows, and the box is published: each lane's proxy fence, the
-// warp barrier, and lane 0's arrival with release semantics on the even CTA's v_full.  Out of line:
-// it runs at most twice per segment (four times with a window).  False if the wait failed.
-__device__ __noinline__ bool tc_finish_ragged_v(uint8_t* box, uint64_t* fix, uint32_t fix_phase, int rank, TcBox bx,
+// warp barrier, and lane 0's release of shared memory and arrival on the even CTA's v_full.  Out of
+// line: it runs at most twice per segment (four times with a window).  False if the wait failed.
+__device__ __noinline__ bool tc_finish_ragged_v(uint8_t* box, uint64_t* fix, uint32_t fix_phase, TcBox bx,
                                                 uint32_t vfull, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
   int ok = 1;
@@ -304,10 +272,8 @@ __device__ __noinline__ bool tc_finish_ragged_v(uint8_t* box, uint64_t* fix, uin
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    if (rank == 0)
-      mbar_arrive_expect_tx_addr(vfull, 0u);
-    else
-      mbar_arrive_addr(vfull);
+    fence_release_smem_to_cluster();   // (a release arrival at cluster scope would take about 1 us)
+    mbar_arrive_relaxed(vfull);
   }
   return true;
 }
@@ -320,11 +286,9 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
   const int lane = threadIdx.x & 31;
   const bool l0 = elect_one();
   const bool leader = rank == 0;
-  // Lane 0 waits; the verdict (and an abort seen meanwhile) is shared with the warp.
+  // Every lane waits; the verdict (and an abort seen meanwhile) is shared by the warp.
   auto wait0 = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-    int ok = 1;
-    if (l0) ok = (mbar_wait(bar, parity, site) && !*abort_flag) ? 1 : 0;
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, site) && !*abort_flag);
   };
   SegmentCursor cur{plan.b0, plan.off0, plan.start, plan.end, plan.b_end, pair, true, plan.len0};
   Segment sg;
@@ -333,7 +297,6 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
   int k = 0;    // segment index
   uint32_t fix_phase = 0;
   bool ok = true;
-  PageWindow pw, pw_sinks;   // the sinks' pages have ids of their own: tile 0 looks up both places
   const bool paged = a.v.page_size != 0;
   const Rows rows = tc_rows<Rows>(a);
   while (ok && cur.next(a.seq_lens, a.capacity, rows, sg)) {
@@ -353,19 +316,33 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
       else
         mbar_arrive_relaxed(lbar(&bars->q_full));
     }
-    // TMA row of token t of query row b's sequence (a fully out-of-bounds box for a bad map entry).
-    // Every lane calls it (the paged lookup shares the block ids across the warp).
+    // Where the 64-token box at token t (of the frame; boxes never cross a page) lies: its block id, or its
+    // row in a contiguous cache.  Fetched a tile ahead, so that neither a copy nor the wait before it
+    // stands behind a dependent load of the block table; turned into the TMA row when it is used (a
+    // fully out-of-bounds box for a bad block id or map entry).
     const int cb = tc_cache_seq<kMapped>(a, b, !kV);
-    auto row_of = [&](int t) -> int {
-      if (kMapped && cb < 0) return -kTcTile;
-      if (!paged) return tma_row(a.v, cb, map.real(t));
-      if (Rows::kHoles && map.in_sinks(t)) return pw_row(pw_sinks, a.v, cb, t, lane);
-      return pw_row(pw, a.v, cb, map.real(t), lane);
+    const int32_t* table = paged ? a.v.block_table + static_cast<int64_t>(cb < 0 ? 0 : cb) * a.v.max_blocks : nullptr;
+    auto fetch = [&](int t) -> int {
+      if (kMapped && cb < 0) return INT_MIN;
+      const int r = map.real(t);
+      return paged ? table[r / kPage] : static_cast<int>(cache_row(a.v, cb, r));
     };
+    auto row_of = [&](int id) -> int {
+      if (!paged || id == INT_MIN) return id < 0 ? -kTcTile : id;
+      const int64_t r = static_cast<int64_t>(id) * kPage;
+      if (id < 0 || r >= a.v.num_rows) {
+        if (l0) set_dev_error(0x2);
+        return -kTcTile;
+      }
+      return static_cast<int>(r);
+    };
+    auto k_token = [&](int i) { return t_begin + i * kTcTile + 64 * static_cast<int>(rank); };
+    int k_id = 0;
+    if (!kV && k_token(0) < t_end) k_id = fetch(k_token(0));
     auto issue_k = [&](int i) -> bool {
       const int gi = g + i;
-      const int my0 = t_begin + i * kTcTile + 64 * static_cast<int>(rank);
-      const int y = my0 < t_end ? row_of(my0) : -kTcTile;
+      const int y = k_token(i) < t_end ? row_of(k_id) : -kTcTile;
+      if (k_token(i + 1) < t_end) k_id = fetch(k_token(i + 1));
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {
         if (gi >= 1 && !wait0(&bars->k_empty[part], static_cast<uint32_t>(gi - 1) & 1u, 0x10 + part)) return false;
@@ -389,13 +366,27 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
       }
       return true;
     };
+    int v_id[2];
+    auto fetch_v = [&](int i) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int tok0 = t_begin + i * kTcTile + 64 * s;
+        if (tok0 < t_end) v_id[s] = fetch(tok0);
+      }
+    };
+    if (kV) fetch_v(0);
     auto issue_v = [&](int i) -> bool {
       TcBox bx[2];
+      int rows2[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bx[s] = tc_box<Rows::kHoles>(map, t_begin + i * kTcTile + 64 * s, t_end);
+        rows2[s] = bx[s].valid > 0 ? row_of(v_id[s]) : 0;
+      }
+      if (i + 1 < n_tiles) fetch_v(i + 1);
 #pragma unroll
       for (int s = 0; s < 2; ++s, ++vn) {   // box h of a tile sits in slot h
-        const int tok0 = t_begin + i * kTcTile + 64 * s;
-        bx[s] = tc_box<Rows::kHoles>(map, tok0, t_end);
-        const int row = bx[s].valid > 0 ? row_of(tok0) : 0;   // before the wait, which hides the lookup
+        const int row = rows2[s];
         if (vn >= kTcVSlots && !wait0(&bars->v_empty[s], static_cast<uint32_t>((vn / kTcVSlots) - 1) & 1u, 0x12))
           return false;
         uint8_t* box = smem + kTcOffV + s * kTcVBox;
@@ -432,8 +423,8 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
 #pragma unroll
         for (int s = 0; s < 2; ++s) {   // with both copies on their way
           if (bx[s].valid == 0 || bx[s].whole()) continue;
-          if (!tc_finish_ragged_v(smem + kTcOffV + s * kTcVBox, &bars->fix[s], (fix_phase >> s) & 1u,
-                                  static_cast<int>(rank), bx[s], lbar(&bars->v_full[s]), abort_flag))
+          if (!tc_finish_ragged_v(smem + kTcOffV + s * kTcVBox, &bars->fix[s], (fix_phase >> s) & 1u, bx[s],
+                                  lbar(&bars->v_full[s]), abort_flag))
             return false;
           fix_phase ^= 1u << s;
         }
