@@ -747,35 +747,33 @@ __device__ __noinline__ void tc_write_segment(bool direct, void* row, float* m_o
     const float inv = l_tot > 0.f ? 1.f / l_tot : 0.f;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(row) + lat0;
     uint8_t* row0 = reinterpret_cast<uint8_t*>(dst) - static_cast<size_t>(lane) * kDLat * 2;
-    for (int qb = 0; qb < 2; ++qb) {   // 64 latent columns (128 bytes of bf16) per pass
-      uint32_t r[4][16];
+    // A loop of small bodies, 32 latent columns (64 bytes of bf16) each: the code is cold at every segment.
+#pragma unroll 1
+    for (int qb = 0; qb < 4; ++qb) {
+      uint32_t r[2][16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld16(ocol + 16 * (4 * qb + q), r[q]);
+      for (int q = 0; q < 2; ++q) tmem_ld16(ocol + 32 * qb + 16 * q, r[q]);
       tmem_ld_wait();
-      uint32_t w[32];
+      uint32_t w[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          __nv_bfloat162 h2 =
-              __floats2bfloat162_rn(__uint_as_float(r[q][2 * e]) * inv, __uint_as_float(r[q][2 * e + 1]) * inv);
-          w[8 * q + e] = *reinterpret_cast<uint32_t*>(&h2);
-        }
-      store_rows_64b(stage, w, row0 + 128 * qb, static_cast<size_t>(kDLat) * 2, lane);
-      store_rows_64b(stage, w + 16, row0 + 128 * qb + 64, static_cast<size_t>(kDLat) * 2, lane);
+      for (int e = 0; e < 16; ++e) {
+        __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(r[e >> 3][2 * (e & 7)]) * inv,
+                                                  __uint_as_float(r[e >> 3][2 * (e & 7) + 1]) * inv);
+        w[e] = *reinterpret_cast<uint32_t*>(&h2);
+      }
+      store_rows_64b(stage, w, row0 + 64 * qb, static_cast<size_t>(kDLat) * 2, lane);
     }
     if (half == 0 && ch == 0 && m_or_lse != nullptr)
       *m_or_lse = l_tot > 0.f ? (m_used + log2f(l_tot)) * kLn2 : -INFINITY;
   } else {
     float* dst = static_cast<float*>(row) + lat0;
     uint8_t* row0 = reinterpret_cast<uint8_t*>(dst) - static_cast<size_t>(lane) * kDLat * 4;
-    for (int qb = 0; qb < 4; ++qb) {   // 32 latent columns (128 bytes of fp32) per pass
-      uint32_t w[32];
-      tmem_ld16(ocol + 32 * qb, *reinterpret_cast<uint32_t(*)[16]>(&w[0]));
-      tmem_ld16(ocol + 32 * qb + 16, *reinterpret_cast<uint32_t(*)[16]>(&w[16]));
+#pragma unroll 1
+    for (int qb = 0; qb < 8; ++qb) {   // 16 latent columns (64 bytes of fp32) each
+      uint32_t w[16];
+      tmem_ld16(ocol + 16 * qb, w);
       tmem_ld_wait();
-      store_rows_64b(stage, w, row0 + 128 * qb, static_cast<size_t>(kDLat) * 4, lane);
-      store_rows_64b(stage, w + 16, row0 + 128 * qb + 64, static_cast<size_t>(kDLat) * 4, lane);
+      store_rows_64b(stage, w, row0 + 64 * qb, static_cast<size_t>(kDLat) * 4, lane);
     }
     if (half == 0 && ch == 0) {
       *m_or_lse = m_used;
