@@ -283,7 +283,6 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
                             const CUtensorMap* tm_q, const CUtensorMap* tm_sc, const DecodeTcArgs& a,
                             const TcPlan& plan, uint8_t* smem, TcBars* bars, uint32_t rank, int pair,
                             volatile int* abort_flag) {
-  const int lane = threadIdx.x & 31;
   const bool l0 = elect_one();
   const bool leader = rank == 0;
   // Every lane waits; the verdict (and an abort seen meanwhile) is shared by the warp.

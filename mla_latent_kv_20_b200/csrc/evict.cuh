@@ -17,10 +17,11 @@
 
 namespace mla {
 
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvKeys = 16384;        // order keys a CTA holds in shared memory (a longer slice is read again)
 constexpr int kEvMaxCluster = 8;
+constexpr int kEvCopies = 8;         // of each counter of a histogram
 
 // Workspace: the kept tokens' weights [batch][keep] fp32 and the lengths before the eviction [batch].
 // The move kernel reads these alone, so weights_out may be weights, and lens_out seq_lens.
@@ -40,12 +41,12 @@ __host__ __device__ __forceinline__ size_t ev_ws_bytes(int batch, int keep) {
 
 struct EvSmem {
   uint32_t keys[kEvKeys];
-  uint32_t hist[256 * 32];        // [digit][lane]: the lanes of a warp never meet in a bank or a counter
+  uint32_t hist[256 * kEvCopies]; // [digit][lane % 8]: at most four lanes of a warp meet in a counter
   uint32_t total[2][256];         // this CTA's histogram, read by the cluster (two passes alternate)
-  uint32_t sums[256];             // the cluster's
+  uint32_t sums[256];             // the cluster's (clusters of more than one CTA)
   uint32_t count[2];              // this CTA's keys above and at the threshold, read by the cluster
-  uint32_t warp_gt[kEvWarps], warp_eq[kEvWarps];
-  uint32_t digit, above;
+  uint32_t warp_gt[32], warp_eq[32];   // (the warps there are, then zeros)
+  uint32_t digit, above, same;
 };
 
 // Weights in order as unsigned numbers: -inf < ... < -0 = 0 < ... < inf, and NaN (0) below them all.
@@ -90,55 +91,69 @@ __global__ void __launch_bounds__(kEvThreads, 1)
     }
     return;
   }
-  for (int j = me; j < sinks; j += all) {
-    kp[j] = j;
-    kw[j] = w[j];
-  }
-  for (int j = me; j < recent; j += all) {
-    kp[keep - recent + j] = L - recent + j;
-    kw[keep - recent + j] = w[L - recent + j];
-  }
+  auto write_sure = [&](int from, int step) {   // the tokens that are kept whatever they weigh
+    for (int j = from; j < sinks + recent; j += step) {
+      const int to = j < sinks ? j : keep - recent + (j - sinks), t = j < sinks ? j : L - recent + (j - sinks);
+      kp[to] = t;
+      kw[to] = w[t];
+    }
+  };
   const int k = keep - sinks - recent;
-  if (k == 0) return;
+  if (k == 0) {
+    write_sure(me, all);
+    return;
+  }
   // This CTA's slice of the middle, in order: tokens first + [0, n).
   const int M = L - sinks - recent;   // > k
   const int S = (M + C - 1) / C;
   const int first = sinks + min(M, rank * S);
   const int n = min(M - min(M, rank * S), S);
-  for (int i = tid; i < min(n, kEvKeys); i += kEvThreads) sm.keys[i] = ev_key(w[first + i]);
+  for (int i = tid; i < 256 * kEvCopies; i += kEvThreads) sm.hist[i] = 0;
+  if (tid < 32) sm.warp_gt[tid] = sm.warp_eq[tid] = 0;
+  const int held = min(n, kEvKeys);
+  for (int i0 = tid; i0 < held; i0 += 8 * kEvThreads) {   // eight loads in flight
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = i0 + u * kEvThreads < held ? w[first + i0 + u * kEvThreads] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u * kEvThreads < held) sm.keys[i0 + u * kEvThreads] = ev_key(x[u]);
+  }
   auto key_at = [&](int i) { return i < kEvKeys ? sm.keys[i] : ev_key(w[first + i]); };
 
-  uint32_t prefix = 0, k_rem = static_cast<uint32_t>(k);
-  for (int pass = 0; pass < 4; ++pass) {
+  // Digit by digit from the top.  `prefix` holds the digits found, k_rem how many of the keys that share
+  // them are kept.  Done before the last digit if that is all of them.
+  uint32_t prefix = 0, k_rem = static_cast<uint32_t>(k), thr = 0;
+  for (int pass = 0;; ++pass) {
     const int shift = 24 - 8 * pass;
-    for (int i = tid; i < 256 * 32; i += kEvThreads) sm.hist[i] = 0;
-    __syncthreads();
+    __syncthreads();   // the counters are zero
     for (int i = tid; i < n; i += kEvThreads) {
       const uint32_t key = key_at(i);
-      if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&sm.hist[((key >> shift) & 255u) * 32 + lane], 1u);
+      if (pass == 0 || (key >> (shift + 8)) == prefix)
+        atomicAdd(&sm.hist[((key >> shift) & 255u) * kEvCopies + (lane & (kEvCopies - 1))], 1u);
     }
     __syncthreads();
-    {   // digit d summed by four threads, eight counters each, every one from a bank of its own
-      const int d = tid >> 2, q = tid & 3;
+    if (tid < 256) {   // digit tid: its copies lie in different banks for the lanes of a warp
       uint32_t s = 0;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s += sm.hist[d * 32 + ((8 * q + u + d) & 31)];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (q == 0) sm.total[pass & 1][d] = s;
+      for (int u = 0; u < kEvCopies; ++u) s += sm.hist[tid * kEvCopies + ((u + (tid >> 2)) & (kEvCopies - 1))];
+      sm.total[pass & 1][tid] = s;
     }
-    cluster_sync();
-    if (tid < 256) {
-      uint32_t s = 0;
-      for (int c = 0; c < C; ++c) s += ld_dsmem_u32(&sm.total[pass & 1][tid], c);
-      sm.sums[tid] = s;
+    if (C > 1) {
+      cluster_sync();
+      if (tid < 256) {
+        uint32_t s = 0;
+        for (int c = 0; c < C; ++c) s += ld_dsmem_u32(&sm.total[pass & 1][tid], c);
+        sm.sums[tid] = s;
+      }
     }
     __syncthreads();
     if (warp == 0) {   // the digit of the k-th largest: lane l takes digits 255 - 8 l .. 248 - 8 l
+      const uint32_t* sums = C > 1 ? sm.sums : sm.total[pass & 1];
       uint32_t c8[8], s = 0;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        c8[u] = sm.sums[255 - 8 * lane - u];
+        c8[u] = sums[255 - 8 * lane - u];
         s += c8[u];
       }
       uint32_t incl = s;
@@ -148,29 +163,53 @@ __global__ void __launch_bounds__(kEvThreads, 1)
         if (lane >= o) incl += x;
       }
       uint32_t above = incl - s;
-      if (above < k_rem && incl >= k_rem) {
-        int u = 0;
-        while (above + c8[u] < k_rem) above += c8[u++];
-        sm.digit = 255u - 8u * lane - u;
+      if (above < k_rem && incl >= k_rem) {   // one lane
+        uint32_t digit = 255u - 8u * lane, same = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (same == 0) {
+            if (above + c8[u] >= k_rem) {
+              same = c8[u];
+              digit -= u;
+            } else {
+              above += c8[u];
+            }
+          }
+        }
+        sm.digit = digit;
         sm.above = above;
+        sm.same = same;
       }
+    } else {
+      for (int i = tid - 32; i < 256 * kEvCopies; i += kEvThreads - 32) sm.hist[i] = 0;
+      if (pass == 0) write_sure(rank * (kEvThreads - 32) + tid - 32, C * (kEvThreads - 32));
     }
     __syncthreads();
     prefix = (prefix << 8) | sm.digit;
     k_rem -= sm.above;
+    // Keys above thr are kept, and the first k_rem of those equal to it.
+    if (k_rem == sm.same) {           // all that share the digits: the ones above the largest key below these
+      thr = (prefix << shift) - 1u;   // (not below 0: with k < M some key is smaller)
+      k_rem = 0;
+      break;
+    }
+    if (pass == 3) {
+      thr = prefix;
+      break;
+    }
   }
-  const uint32_t thr = prefix;   // keys above it are kept, and the first k_rem of those equal to it
 
   // Number the kept tokens: warp w walks its part of the slice in order, 32 at a time.
   const int per = ((n + kEvWarps - 1) / kEvWarps + 31) & ~31;
   const int lo = min(n, warp * per), hi = min(n, lo + per);
   uint32_t gt = 0, eq = 0;
-  for (int i = lo; i < hi; i += 32) {
-    const bool in = i + lane < hi;
-    const uint32_t key = in ? key_at(i + lane) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, in && key > thr));
-    eq += __popc(__ballot_sync(0xffffffffu, in && key == thr));
+  for (int i = lo + lane; i < hi; i += 32) {
+    const uint32_t key = key_at(i);
+    gt += key > thr;
+    eq += key == thr;
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     sm.warp_gt[warp] = gt;
     sm.warp_eq[warp] = eq;
@@ -193,29 +232,36 @@ __global__ void __launch_bounds__(kEvThreads, 1)
     sm.warp_gt[lane] = g - sm.warp_gt[lane];   // before this warp, within the slice
     sm.warp_eq[lane] = e - sm.warp_eq[lane];
   }
-  cluster_sync();
+  if (C > 1) cluster_sync();
+  else __syncthreads();
   uint32_t g0 = sm.warp_gt[warp], e0 = sm.warp_eq[warp];
   for (int c = 0; c < rank; ++c) {
     g0 += ld_dsmem_u32(&sm.count[0], c);
     e0 += ld_dsmem_u32(&sm.count[1], c);
   }
   const uint32_t below = (1u << lane) - 1u;
-  for (int i = lo; i < hi; i += 32) {
-    const bool in = i + lane < hi;
-    const uint32_t key = in ? key_at(i + lane) : 0u;
-    const uint32_t bg = __ballot_sync(0xffffffffu, in && key > thr);
-    const uint32_t be = __ballot_sync(0xffffffffu, in && key == thr);
-    const uint32_t e = e0 + __popc(be & below);
-    if (in && (key > thr || (key == thr && e < k_rem))) {
-      const int j = sinks + static_cast<int>(g0 + __popc(bg & below) + min(e, k_rem));
-      const int t = first + i + lane;
-      kp[j] = t;
-      kw[j] = w[t];
+  constexpr int kAhead = 4;
+  for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {
+    float x[kAhead];   // the weights themselves are written too
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) x[u] = i0 + 32 * u + lane < hi ? w[first + i0 + 32 * u + lane] : 0.f;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + 32 * u + lane;
+      const uint32_t key = ev_key(x[u]);
+      const bool above = i < hi && key > thr, equal = i < hi && key == thr;
+      const uint32_t bg = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
+      const uint32_t e = e0 + __popc(be & below);
+      if (above || (equal && e < k_rem)) {
+        const int j = sinks + static_cast<int>(g0 + __popc(bg & below) + min(e, k_rem));
+        kp[j] = first + i;
+        kw[j] = x[u];
+      }
+      g0 += __popc(bg);
+      e0 += __popc(be);
     }
-    g0 += __popc(bg);
-    e0 += __popc(be);
   }
-  cluster_sync();   // no CTA leaves while another reads its counts
+  if (C > 1) cluster_sync();   // no CTA leaves while another reads its counts
 }
 
 // A cache of rows of `row_bytes` bytes (1152 bf16, 576 FP8) with, for FP8, a scale byte per row.
