@@ -52,6 +52,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 //   O      [2P][128][512] fp32   (unnormalised partial sums of c)
 //   m      [2P][128]      fp32   (running max, log2 domain)
 //   l      [2P][128]      fp32   (running sum of exp2(s - m))
+//   split  [P]            int32  (the row whose first piece range p holds if that row is split, else -1)
 //   plan   [batch + 2]    int32  (balanced: cost prefix W_b of each sequence, [batch] = C;
 //                                 per sequence: first range of each sequence, [batch] = ranges used;
 //                                 [batch + 1] = the plan kind)
@@ -59,6 +60,7 @@ struct Workspace {
   float* o;
   float* m;
   float* l;
+  int32_t* split;
   int32_t* off;
 };
 __host__ __device__ __forceinline__ Workspace ws_carve(void* base, int P) {
@@ -66,12 +68,13 @@ __host__ __device__ __forceinline__ Workspace ws_carve(void* base, int P) {
   w.o = reinterpret_cast<float*>(base);
   w.m = w.o + static_cast<int64_t>(2 * P) * kHeads * kDLat;
   w.l = w.m + static_cast<int64_t>(2 * P) * kHeads;
-  w.off = reinterpret_cast<int32_t*>(w.l + static_cast<int64_t>(2 * P) * kHeads);
+  w.split = reinterpret_cast<int32_t*>(w.l + static_cast<int64_t>(2 * P) * kHeads);
+  w.off = w.split + P;
   return w;
 }
 __host__ __device__ __forceinline__ size_t ws_bytes(int batch, int P) {
   const size_t partials = static_cast<size_t>(2 * P) * kHeads * (kDLat + 2) * sizeof(float);
-  return partials + ((static_cast<size_t>(batch) + 2) * sizeof(int32_t) + 15) / 16 * 16;
+  return partials + ((static_cast<size_t>(batch) + 2 + P) * sizeof(int32_t) + 15) / 16 * 16;
 }
 
 // Effective length of sequence b: seq_lens[b] clamped to [0, capacity] (error word set if it
@@ -202,110 +205,140 @@ struct SegmentCursor {
   }
 };
 
-// Combine: one warp per (b, h) at a time; lanes own 16 of the 512 latent columns.  grid = (batch,
-// 128 / (4 hpw)), block = 128: warp w of block (b, y) takes heads 4 hpw y + w hpw + [0, hpw), so the
-// row's plan entries are read once for hpw heads (hpw = 1 for decode batches; 8 for many rows, as in
-// a prefill, where most rows are finished by the decode kernel and the blocks only read the plan).
-// At most 64 registers a thread for hpw = 1 (8 blocks per SM: a 32-sequence batch is one wave),
-// 128 otherwise.  Empty rows get out_lat = 0 and lse = -inf; rows finished by the decode kernel
-// (one segment) are skipped; the others merge their partials in ascending range order.
-template <int hpw>
-__global__ void __launch_bounds__(128, hpw == 1 ? 8 : 4) combine_kernel(Workspace ws, int P, __nv_bfloat16* __restrict__ out_lat,
+// Combine: merges the partials of split rows and writes the empty ones (out_lat = 0, lse = -inf).
+//   out = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p,   M = max_p m_p,   in ascending range order.
+// kByRange: block x < P takes the row whose first piece range x holds, if it is split (fewer rows are split
+// than there are ranges), and the blocks from P on look over 32 rows each for empty ones; otherwise block
+// x takes row x.  A warp covers 128 kCols latent columns of a head (a lane kCols pieces of four), a block
+// of four warps kCols heads: kCols = 4 where there are rows enough to fill the device, 1 where few rows
+// may have many partials each.  8 / kCols partials are in flight at a time; their m and l are read by
+// lane i for the row's i-th range, 32 ranges at once.
+template <int kCols, bool kByRange>
+__global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int P, int B, __nv_bfloat16* __restrict__ out_lat,
                                                       float* __restrict__ lse) {
+  constexpr int kAhead = 8 / kCols;
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x;
-  const int h0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * hpw;
   const int lane = threadIdx.x & 31;
-  const int B = gridDim.x;
-  const bool per_seq = ws.off[B + 1] == kPlanPerSequence;
-  const int off = ws.off[b];
-  const int span = ws.off[b + 1] - off;   // kSegCost + tiles (balanced) or ranges (per sequence) of b
-  if (span == 0) {
-    for (int h = h0; h < h0 + hpw; ++h) {
-      __nv_bfloat16* dst = out_lat + (static_cast<int64_t>(b) * kHeads + h) * kDLat;
-      for (int i = lane; i < kDLat / 8; i += 32) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
-      if (lse != nullptr && lane == 0) lse[static_cast<int64_t>(b) * kHeads + h] = -INFINITY;
-    }
-    return;
-  }
-  // Ranges [p0, p1] that hold pieces of b; in the per-sequence plan each holds one (slot 2p).
-  // Ranges [p0, p1] that hold pieces of b; in the per-sequence plan each holds one (slot 2p); in
-  // the balanced plan those holding its first and last tiles, at costs off + kSegCost and off + span - 1.
-  const int C = ws.off[B];
-  const int p0 = per_seq ? off : range_of_cost(off + kSegCost, P, C);
-  const int p1 = per_seq ? off + span - 1 : range_of_cost(off + span - 1, P, C);
-  if (p0 == p1) return;
-  // The merge over the ranges, with the slot and emptiness of range p given by the plan kind (two
-  // copies of the loop, so that each keeps only what its kind needs live).
-  auto merge_rows = [&](auto slot_of, auto nonempty) {
-#pragma unroll 1
-    for (int h = h0; h < h0 + hpw; ++h) {
-      __nv_bfloat16* dst = out_lat + (static_cast<int64_t>(b) * kHeads + h) * kDLat;
-      // Online merge in ascending range order: after each range, (M, den, acc) hold the merge of the
-      // ranges so far relative to M.  Two ranges are fetched per step so their loads overlap (every
-      // partial's m is finite: a non-empty range holds at least one valid token of b).
-      float M = -INFINITY, den = 0.f;
-      float acc[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-      auto fetch = [&](int p, float& m, float& l, float4 (&o)[4]) -> bool {
-        if (p > p1 || !nonempty(p)) return false;
-        const int64_t ml = static_cast<int64_t>(slot_of(p)) * kHeads + h;
-        m = ws.m[ml];
-        l = ws.l[ml];
-        const float4* src = reinterpret_cast<const float4*>(ws.o + ml * kDLat);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = src[lane + 32 * i];
-        return true;
-      };
-      auto merge = [&](float m, float l, const float4 (&o)[4]) {
-        const float Mn = fmaxf(M, m);
-        const float sa = M == -INFINITY ? 0.f : exp2f(M - Mn);
-        const float w = exp2f(m - Mn);
-        den = den * sa + w * l;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[4 * i + 0] = acc[4 * i + 0] * sa + w * o[i].x;
-          acc[4 * i + 1] = acc[4 * i + 1] * sa + w * o[i].y;
-          acc[4 * i + 2] = acc[4 * i + 2] * sa + w * o[i].z;
-          acc[4 * i + 3] = acc[4 * i + 3] * sa + w * o[i].w;
-        }
-        M = Mn;
-      };
-      constexpr int kStep = 2;
-      for (int p = p0; p <= p1; p += kStep) {
-        float m[kStep], l[kStep];
-        float4 o[kStep][4];
-        bool has[kStep];
-#pragma unroll
-        for (int u = 0; u < kStep; ++u) has[u] = fetch(p + u, m[u], l[u], o[u]);
-#pragma unroll
-        for (int u = 0; u < kStep; ++u)
-          if (has[u]) merge(m[u], l[u], o[u]);
-      }
-      const float inv = den > 0.f ? 1.f / den : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 lo = __floats2bfloat162_rn(acc[4 * i + 0] * inv, acc[4 * i + 1] * inv);
-        __nv_bfloat162 hi = __floats2bfloat162_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
-        uint2 pk;
-        pk.x = *reinterpret_cast<uint32_t*>(&lo);
-        pk.y = *reinterpret_cast<uint32_t*>(&hi);
-        reinterpret_cast<uint2*>(dst)[lane + 32 * i] = pk;
-      }
-      if (lse != nullptr && lane == 0)
-        lse[static_cast<int64_t>(b) * kHeads + h] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
-    }
+  const int warp = threadIdx.x >> 5;
+  auto write_empty = [&](int b) {
+    const int64_t row = static_cast<int64_t>(b) * kHeads;
+    for (int i = threadIdx.x; i < kHeads * kDLat / 8; i += 128)
+      reinterpret_cast<uint4*>(out_lat + row * kDLat)[i] = make_uint4(0, 0, 0, 0);
+    if (lse != nullptr) lse[row + threadIdx.x] = -INFINITY;
   };
-  if (per_seq) {
-    merge_rows([](int p) { return 2 * p; }, [](int) { return true; });   // one piece per range: slot 2p
-  } else {
-    // Range p began before b (b is not its first segment: slot 2p + 1) when x_p < W_b = off, and is
-    // empty when x_{p+1} = x_p (then the kernel wrote nothing for it).
-    merge_rows([&](int p) { return muldiv(p, C, P) < off ? 2 * p + 1 : 2 * p; },
-               [&](int p) { return muldiv(p, C, P) < muldiv(p + 1, C, P); });
+  int b = blockIdx.x, p0;
+  if (kByRange) {
+    if (blockIdx.x >= P) {
+      if (blockIdx.y != 0) return;
+      const int b0 = 32 * (static_cast<int>(blockIdx.x) - P);
+      uint32_t empty = __ballot_sync(0xffffffffu, b0 + lane < B && ws.off[b0 + lane + 1] == ws.off[b0 + lane]);
+      for (; empty != 0; empty &= empty - 1) write_empty(b0 + __ffs(empty) - 1);
+      return;
+    }
+    p0 = blockIdx.x;
+    b = ws.split[p0];
+    if (b < 0) return;
   }
+  // Ranges [p0, p1] hold b's pieces; in the per-sequence plan each holds one (slot 2p).  In the balanced
+  // plan they are those that hold its first and last tiles, at costs off + kSegCost and off + span - 1;
+  // a piece is the range's last segment (slot 2p + 1) where the range began before b, x_p < W_b = off,
+  // and a range with x_p = x_{p+1} is empty.
+  const bool per_seq = ws.off[B + 1] == kPlanPerSequence;
+  const int off = ws.off[b], span = ws.off[b + 1] - off, C = ws.off[B];
+  if (!kByRange) {
+    if (span == 0) {
+      if (blockIdx.y == 0) write_empty(b);
+      return;
+    }
+    p0 = per_seq ? off : range_of_cost(off + kSegCost, P, C);
+  }
+  const int p1 = per_seq ? off + span - 1 : range_of_cost(off + span - 1, P, C);
+  if (p0 == p1) return;   // finished by the decode kernel
+  const int h = blockIdx.y * kCols + (kCols == 4 ? warp : 0);
+  const int col = 4 * lane + (kCols == 4 ? 0 : 128 * warp);
+  float M = -INFINITY, den = 0.f;
+  float4 acc[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int pc = p0; pc <= p1; pc += 32) {   // 32 ranges at a time, this lane's first
+    const int p = pc + lane;
+    int slot = -1;
+    if (p <= p1) {
+      if (per_seq) {
+        slot = 2 * p;
+      } else {
+        const int x = muldiv(p, C, P);
+        if (x < muldiv(p + 1, C, P)) slot = x < off ? 2 * p + 1 : 2 * p;
+      }
+    }
+    float m = -INFINITY, l = 0.f;
+    if (slot >= 0) {
+      m = ws.m[static_cast<int64_t>(slot) * kHeads + h];
+      l = ws.l[static_cast<int64_t>(slot) * kHeads + h];
+    }
+    float4 o[kAhead][kCols];
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int sl = __shfl_sync(0xffffffffu, slot, i0 + u);
+        const float* src = ws.o + (static_cast<int64_t>(sl) * kHeads + h) * kDLat + col;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          o[u][c] = sl >= 0 ? *reinterpret_cast<const float4*>(src + 128 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    fetch(0);
+    float top = m;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float Mn = fmaxf(M, top);   // finite: a non-empty range holds at least one valid token of b
+    const float sa = M == -INFINITY ? 0.f : exp2f(M - Mn);
+    const float w = slot >= 0 ? exp2f(m - Mn) : 0.f;
+    float wl = w * l;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, d);
+    den = den * sa + wl;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      acc[c].x *= sa;
+      acc[c].y *= sa;
+      acc[c].z *= sa;
+      acc[c].w *= sa;
+    }
+    M = Mn;
+    const int cnt = min(32, p1 - pc + 1);
+#pragma unroll 1
+    for (int i0 = 0;;) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, i0 + u);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          acc[c].x = fmaf(wu, o[u][c].x, acc[c].x);
+          acc[c].y = fmaf(wu, o[u][c].y, acc[c].y);
+          acc[c].z = fmaf(wu, o[u][c].z, acc[c].z);
+          acc[c].w = fmaf(wu, o[u][c].w, acc[c].w);
+        }
+      }
+      if ((i0 += kAhead) >= cnt) break;
+      fetch(i0);
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const int64_t bh = static_cast<int64_t>(b) * kHeads + h;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+    uint2 pk;
+    pk.x = *reinterpret_cast<const uint32_t*>(&lo);
+    pk.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(out_lat + bh * kDLat + col + 128 * c) = pk;
+  }
+  if (lse != nullptr && lane == 0 && (kCols == 4 || warp == 0))
+    lse[bh] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
 }  // namespace mla

@@ -201,12 +201,16 @@ mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t*
   mla_status ls = launch_chained(kernel, dim3(2 * P), dim3(mla::tc_threads(fp8)),
                                  static_cast<size_t>(mla::kTcSmemBytes), s, tka, tkb, tv, tq, tsc, a);
   if (ls != MLA_OK) return ls;
-  // Many rows (a prefill): each warp takes 8 heads of its row, so the plan is read by 8x fewer blocks.
-  if (rows > 512)
-    return launch_chained(mla::combine_kernel<8>, dim3(rows, mla::kHeads / 32), dim3(128), 0, s, a.ws, P,
-                          reinterpret_cast<__nv_bfloat16*>(out_lat), lse);
-  return launch_chained(mla::combine_kernel<1>, dim3(rows, mla::kHeads / 4), dim3(128), 0, s, a.ws, P,
-                        reinterpret_cast<__nv_bfloat16*>(out_lat), lse);
+  if (P == 1) return MLA_OK;   // one range covers every row
+  auto* out = reinterpret_cast<__nv_bfloat16*>(out_lat);
+  if (rows <= 8)   // few rows, perhaps of many partials
+    return launch_chained(mla::combine_kernel<1, false>, dim3(rows, mla::kHeads), dim3(128), 0, s, a.ws, P, rows, out,
+                          lse);
+  if (rows <= 2 * P)
+    return launch_chained(mla::combine_kernel<4, false>, dim3(rows, mla::kHeads / 4), dim3(128), 0, s, a.ws, P, rows,
+                          out, lse);
+  return launch_chained(mla::combine_kernel<4, true>, dim3(P + (rows + 31) / 32, mla::kHeads / 4), dim3(128), 0, s, a.ws,
+                        P, rows, out, lse);
 }
 
 }  // namespace

@@ -842,6 +842,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       }
     }
   };
+  int split_row = -1;   // the split row whose first piece this range holds (at most one), for the combine
   bool more = cur.next(a.seq_lens, a.capacity, rows, sg);
   while (more) {
   const auto map = rows.map(sg.len);
@@ -990,10 +991,25 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   done.direct = sg.direct;
   done.m = m_used;
   done.l = l_run;
+  if (!sg.direct && sg.tok_begin == 0) split_row = sg.b;
   ++k;
   more = cur.next(a.seq_lens, a.capacity, rows, sg);
   }
   if (ok && k > 0) epilogue(k - 1, red + (g & 1) * 256);   // the buffer the last tile did not use
+  if (rank == 0 && threadIdx.x == 0) a.ws.split[pair] = split_row;
+}
+
+// A call of one range has no split rows and is not followed by a combine: its empty rows are written here.
+template <class Rows>
+__device__ void tc_empty_rows(const DecodeTcArgs& a, uint32_t rank) {
+  const Rows rows = tc_rows<Rows>(a);
+  for (int b = 0; b < a.batch; ++b) {
+    if (rows.span(seq_len_checked(a.seq_lens, b, a.capacity)) != 0) continue;
+    const int64_t row = static_cast<int64_t>(b) * kHeads + 64 * static_cast<int>(rank);
+    for (int i = threadIdx.x; i < 64 * kDLat / 8; i += 32 * kTcSoftmaxWarps)
+      reinterpret_cast<uint4*>(a.out_lat + row * kDLat)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse != nullptr && threadIdx.x < 64) a.lse[row + threadIdx.x] = -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------------------ work plan
@@ -1255,8 +1271,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
   const bool busy = pl.start < pl.end;   // the same in both CTAs of the pair
   const uint32_t tmem = *tmem_slot;
 
-  if (!busy) {
-    // an idle range: only the teardown below
+  if (warp < kTcSoftmaxWarps && a.P == 1) tc_empty_rows<Rows>(a, rank);
+  if (!busy) {   // an idle range: only the teardown below
+    if (rank == 0 && threadIdx.x == 0) a.ws.split[pair] = -1;
   } else if (warp < kTcSoftmaxWarps) {
     tc_softmax<kMapped, Rows>(a, pl, pair, smem, bars, red, tmem, rank, abort_flag);
   } else if (warp == kTcProducerWarp || warp == kTcVProducerWarp) {
