@@ -227,6 +227,8 @@ __global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int P, int B
       reinterpret_cast<uint4*>(out_lat + row * kDLat)[i] = make_uint4(0, 0, 0, 0);
     if (lse != nullptr) lse[row + threadIdx.x] = -INFINITY;
   };
+  const bool per_seq = ws.off[B + 1] == kPlanPerSequence;
+  const int C = ws.off[B];
   int b = blockIdx.x, p0;
   if (kByRange) {
     if (blockIdx.x >= P) {
@@ -244,8 +246,7 @@ __global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int P, int B
   // plan they are those that hold its first and last tiles, at costs off + kSegCost and off + span - 1;
   // a piece is the range's last segment (slot 2p + 1) where the range began before b, x_p < W_b = off,
   // and a range with x_p = x_{p+1} is empty.
-  const bool per_seq = ws.off[B + 1] == kPlanPerSequence;
-  const int off = ws.off[b], span = ws.off[b + 1] - off, C = ws.off[B];
+  const int off = ws.off[b], span = ws.off[b + 1] - off;
   if (!kByRange) {
     if (span == 0) {
       if (blockIdx.y == 0) write_empty(b);

@@ -206,7 +206,7 @@ mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t*
   if (rows <= 8)   // few rows, perhaps of many partials
     return launch_chained(mla::combine_kernel<1, false>, dim3(rows, mla::kHeads), dim3(128), 0, s, a.ws, P, rows, out,
                           lse);
-  if (rows <= 2 * P)
+  if (rows <= P)
     return launch_chained(mla::combine_kernel<4, false>, dim3(rows, mla::kHeads / 4), dim3(128), 0, s, a.ws, P, rows,
                           out, lse);
   return launch_chained(mla::combine_kernel<4, true>, dim3(P + (rows + 31) / 32, mla::kHeads / 4), dim3(128), 0, s, a.ws,
