@@ -19,9 +19,13 @@
 // copy brings 64 rows x 3 slabs in whole swizzle atoms, and the operand descriptor's 8-row stride spans
 // the three slabs, so two 64-token pages form one 128-row operand.
 //
-// One thread issues a tcgen05.mma of this size about every 125 cycles, twice what the pair needs for
-// it, so two warps issue, each the K steps of its parity into an accumulator of its own (the readers add
-// the two): 2 issuers x 2 buffers x 128 columns = all 512 TMEM columns.
+// TMEM: two S buffers of 128 columns, so a unit's MMAs overlap the exponentials of the one before.
+//
+// What bounds it.  A decode step: HBM.  128 sequences of 1024..8192 tokens in pages (670 MB, none of it in L2)
+// take 127 us, 5.3 TB/s, 0.82 of the measured copy rate; of these about 7 us go before the first tile's
+// scores.  A chunk: the tensor pipe; 64 rows of 74 tiles take 113 us, 2620 cycles a unit against the 2304
+// of its 36 MMAs.  FP8: the converters and the slots' round trip (copy, conversion, MMAs, then the next copy,
+// 5500 cycles a unit): 74 x 4096, 59 us.
 //
 // Split.  The units of all sequences (sequence, then tile, then row) are laid end to end and cut into P
 // equal ranges, one per CTA pair.  A tile whose rows fall into several ranges leaves partial sums in the
@@ -54,10 +58,11 @@ constexpr int kAwOffMisc = kAwOffBar + 512;
 constexpr int kAwSmemBytes = kAwOffMisc + 64;
 static_assert(kAwSmemBytes <= 232448, "shared memory budget");
 
+constexpr uint32_t kAwTmemCols = 256;              // two S buffers x 128 heads
 constexpr int kAwSumWarps = 8;                     // read S, exponentiate, sum
-constexpr int kAwMmaWarp = 8;                      // and the next one
-constexpr int kAwProducerWarp = 10;                // and, bf16, the next two
-constexpr int kAwConvWarp0 = 11;
+constexpr int kAwMmaWarp = 8;
+constexpr int kAwProducerWarp = 9;                 // and, bf16, the next two
+constexpr int kAwConvWarp0 = 10;
 constexpr int kAwConvThreads = 256;
 __host__ __device__ constexpr int aw_producers(bool fp8) { return fp8 ? 1 : kAwParts; }
 __host__ __device__ constexpr int aw_threads(bool fp8) {
@@ -66,10 +71,10 @@ __host__ __device__ constexpr int aw_threads(bool fp8) {
 
 struct AwBars {
   uint64_t k_full[kAwParts];    // even CTA: both CTAs' part landed (one arrival per CTA + tx)
-  uint64_t k_empty[kAwParts];   // both: the part consumed (one commit per issuer)
+  uint64_t k_empty[kAwParts];   // both: the part consumed
   uint64_t q_full[kAwQParts];
   uint64_t q_empty[kAwQParts];
-  uint64_t s_full[2];           // both: a unit's scores done (one commit per issuer)
+  uint64_t s_full[2];           // both: a unit's scores done
   uint64_t s_empty[2];          // even CTA: every summing warp of both CTAs has read them
   uint64_t kraw[kAwParts];      // FP8, per CTA: the part's codes landed (+ tx)
 };
@@ -92,7 +97,8 @@ struct AwArgs {
   float* weights;
   const uint8_t* scales;    // FP8
   float* part;              // [2 P][kAwTile] partial sums (kRows)
-  int4* rec;                // [2 P] {sequence or -1, tile, first row, end row} of each partial (kRows)
+  int4* rec;                // [2 P] {sequence or -1, tile, first row, end row} of each partial (kRows); the sign
+                            // bit of the end row marks the tile's last piece
 };
 
 // Workspace of the chunk form: partial sums, then their records.
@@ -135,6 +141,7 @@ __device__ __noinline__ AwPlan aw_make_plan(const AwArgs& a, int pair) {
   const int per = (a.batch + 31) / 32;
   const int lo = min(a.batch, lane * per), hi = min(a.batch, lo + per);
   long long mine = 0;
+#pragma unroll 4
   for (int b = lo; b < hi; ++b) {
     const AwSeq s = aw_seq<kRows>(a, b);
     mine += static_cast<long long>(s.tiles) * s.R;
@@ -215,9 +222,10 @@ struct AwCursor {
 };
 
 // ------------------------------------------------------------------------------ TMA producers
-// A thread needs about 0.27 us to wait for a slot, announce the bytes and issue the copy, whatever its size
-// (8 KB copies from L2: 30 GB/s per SM from one thread, 111 from four), so a chunk's queries, 9 copies per 1.2 us
-// of MMAs, take three producer warps: warp i copies part i of K and the parts of Q that it covers.
+// A thread needs about 0.2 us to wait for a slot, announce the bytes and issue the copy, whatever its size
+// (8 KB copies from L2: 39 GB/s per SM from one thread, 137 from four), so a chunk's queries take three
+// producer warps: warp i copies part i of K and the part of Q that it covers.  (Nine parts of Q, one slab each,
+// would be refilled sooner, but their handshakes cost the issuer more: 124 -> 182 us for 8 x 32 rows.)
 template <bool kRows, bool kFp8>
 __device__ bool aw_producer(const CUtensorMap* tm_k, const CUtensorMap* tm_q, const AwArgs& a, const AwPlan& plan,
                             uint8_t* smem, AwBars* bars, int rank, int me, volatile int* abort_flag) {
@@ -291,12 +299,12 @@ __device__ bool aw_producer(const CUtensorMap* tm_k, const CUtensorMap* tm_q, co
   return true;
 }
 
-// ------------------------------------------------------------------------------ MMA issuers (even CTA)
-// Issuer j: the 16-deep K steps of parity j of every unit.  A part of K is released with the last row of
+// ------------------------------------------------------------------------------ MMA issuer (even CTA)
+// One elected thread.  A part of K is released with the last row of
 // its segment, a part of Q as soon as another row of the segment follows; the last row's Q is released
 // when the next segment turns out to need another one.
 template <bool kRows>
-__device__ bool aw_mma(uint8_t* smem, AwBars* bars, uint32_t tmem, int j, const AwArgs& a, const AwPlan& plan,
+__device__ bool aw_mma(uint8_t* smem, AwBars* bars, uint32_t tmem, const AwArgs& a, const AwPlan& plan,
                        volatile int* abort_flag) {
   const uint32_t idesc = idesc_bf16_f32(256, 128, false, false);
   const uint64_t dk = sdesc_sw128(smem_u32(smem + kAwOffK), 16, kAwSlabs * 1024);
@@ -316,7 +324,7 @@ __device__ bool aw_mma(uint8_t* smem, AwBars* bars, uint32_t tmem, int j, const 
         for (int i = 0; i < kAwQParts; ++i) umma_commit_pair_mc(&bars->q_empty[i], 3);
       // S buffer u & 1 last held unit u - 2
       if (u >= 2 && !mbar_wait_cluster(&bars->s_empty[u & 1], ((u - 2) >> 1) & 1u, 0x50)) return false;
-      const uint32_t d = tmem + 256 * j + 128 * (u & 1);
+      const uint32_t d = tmem + 128 * (u & 1);
 #pragma unroll
       for (int c = 0; c < 9; ++c) {   // dim-slabs
         const int p = c / kAwSlabs, i = c / kAwQSlabs;
@@ -325,9 +333,9 @@ __device__ bool aw_mma(uint8_t* smem, AwBars* bars, uint32_t tmem, int j, const 
         if (new_q && new_q_part && !mbar_wait_cluster(&bars->q_full[i], ql & 1u, 0x52)) return false;
         if (new_part || new_q_part) tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; kk += 2)
-          umma_bf16_pair(d, sdesc_add(dk, p * kAwKPart + (c % kAwSlabs) * 1024 + 32 * (kk + j)),
-                         sdesc_add(dq, c * kTcSlab + 32 * (kk + j)), idesc, (c | kk) != 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16_pair(d, sdesc_add(dk, p * kAwKPart + (c % kAwSlabs) * 1024 + 32 * kk),
+                         sdesc_add(dq, c * kTcSlab + 32 * kk), idesc, (c | kk) != 0 ? 1u : 0u);
         if (last && (c + 1) % kAwSlabs == 0) umma_commit_pair_mc(&bars->k_empty[p], 3);
         if (!last && (c + 1) % kAwQSlabs == 0) umma_commit_pair_mc(&bars->q_empty[i], 3);
       }
@@ -439,16 +447,14 @@ __device__ void aw_sum(const AwArgs& a, const AwPlan& plan, int pair, uint8_t* s
       if (ok) {
         tc_fence_after();
         const float4* l4 = reinterpret_cast<const float4*>(nl + buf * kHeads + 64 * half);
-        uint32_t ra[2][16], rb[2][16];
+        uint32_t ra[2][16];
         tmem_ld16(addr + 128 * j, ra[0]);
-        tmem_ld16(addr + 256 + 128 * j, rb[0]);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tmem_ld_wait();
           if (c < 3) {
             tmem_ld16(addr + 128 * j + 16 * (c + 1), ra[(c + 1) & 1]);
-            tmem_ld16(addr + 256 + 128 * j + 16 * (c + 1), rb[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
@@ -458,11 +464,10 @@ __device__ void aw_sum(const AwArgs& a, const AwPlan& plan, int pair, uint8_t* s
           for (int e = 0; e < 4; ++e) {
             const float4 l = l4[4 * c + e];
             const uint32_t* x = &ra[c & 1][4 * e];
-            const uint32_t* y = &rb[c & 1][4 * e];
-            sum[0] += ex2_approx(fmaf(__uint_as_float(x[0]) + __uint_as_float(y[0]), scale, l.x));
-            sum[1] += ex2_approx(fmaf(__uint_as_float(x[1]) + __uint_as_float(y[1]), scale, l.y));
-            sum[2] += ex2_approx(fmaf(__uint_as_float(x[2]) + __uint_as_float(y[2]), scale, l.z));
-            sum[3] += ex2_approx(fmaf(__uint_as_float(x[3]) + __uint_as_float(y[3]), scale, l.w));
+            sum[0] += ex2_approx(fmaf(__uint_as_float(x[0]), scale, l.x));
+            sum[1] += ex2_approx(fmaf(__uint_as_float(x[1]), scale, l.y));
+            sum[2] += ex2_approx(fmaf(__uint_as_float(x[2]), scale, l.z));
+            sum[3] += ex2_approx(fmaf(__uint_as_float(x[3]), scale, l.w));
           }
         }
         if (t < lim) acc += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -480,7 +485,8 @@ __device__ void aw_sum(const AwArgs& a, const AwPlan& plan, int pair, uint8_t* s
       } else {   // at most a range's first and last segments
         const int slot = 2 * pair + (seg > 0 ? 1 : 0);
         a.part[static_cast<int64_t>(slot) * kAwTile + 128 * rank + m] = acc;
-        if (m == 0 && rank == 0) a.rec[slot] = make_int4(cur.seg_b, cur.t0 / kAwTile, cur.r0, cur.r1);
+        if (m == 0 && rank == 0)
+          a.rec[slot] = make_int4(cur.seg_b, cur.t0 / kAwTile, cur.r0, cur.r1 | (cur.r1 == cur.s.R ? INT_MIN : 0));
       }
     }
   }
@@ -510,22 +516,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(aw_threads(kFp8), 1)
   if (threadIdx.x == 0) {
     for (int p = 0; p < kAwParts; ++p) {
       mbar_init(&bars->k_full[p], 2);
-      mbar_init(&bars->k_empty[p], 2);
+      mbar_init(&bars->k_empty[p], 1);
       mbar_init(&bars->kraw[p], 1);
     }
     for (int i = 0; i < kAwQParts; ++i) {
       mbar_init(&bars->q_full[i], 2);
-      mbar_init(&bars->q_empty[i], 2);
+      mbar_init(&bars->q_empty[i], 1);
     }
     for (int j = 0; j < 2; ++j) {
-      mbar_init(&bars->s_full[j], 2);
+      mbar_init(&bars->s_full[j], 1);
       mbar_init(&bars->s_empty[j], 2 * kAwSumWarps);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kAwMmaWarp) {
-    tmem_alloc_pair(tmem_slot, 512);
+    tmem_alloc_pair(tmem_slot, kAwTmemCols);
     tmem_relinquish_pair();
   }
   if (warp == kAwProducerWarp && (threadIdx.x & 31) == 0) {
@@ -552,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(aw_threads(kFp8), 1)
   } else if (kFp8 && warp >= kAwConvWarp0) {
     if (!aw_convert<kRows>(a, pl, smem, bars, abort_flag) && threadIdx.x == 32 * kAwConvWarp0) *abort_flag = 1;
   } else if (rank == 0 && elect_one()) {
-    if (!aw_mma<kRows>(smem, bars, tmem, warp - kAwMmaWarp, a, pl, abort_flag)) *abort_flag = 1;
+    if (!aw_mma<kRows>(smem, bars, tmem, a, pl, abort_flag)) *abort_flag = 1;
   }
   __syncwarp();
   if (*reinterpret_cast<volatile int*>(abort_flag)) __nanosleep(200000);   // let stray copies land
@@ -561,33 +567,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(aw_threads(kFp8), 1)
   cluster_sync();
   if (warp == kAwMmaWarp) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, kAwTmemCols);
   }
 }
 
 // The tiles whose rows several ranges share: the block of the range that holds a tile's first row adds
-// the partial sums in range order and writes the weights.  grid = P, block = 256.
+// the partial sums in range order and writes the weights.  grid = P, block = 256.  The records of the next
+// slots are read with the first one's (a tile's pieces lie in neighbouring ranges), so a tile shared by two
+// ranges takes two round trips to memory.
 __global__ void __launch_bounds__(kAwTile) attn_weights_join_kernel(const __grid_constant__ AwArgs a) {
+  constexpr int kNext = 4;
   pdl_trigger();
   pdl_wait();
 #pragma unroll 1
   for (int s = 2 * blockIdx.x; s < 2 * static_cast<int>(blockIdx.x) + 2; ++s) {
-    const int4 first = a.rec[s];
+    int4 rec[kNext];
+#pragma unroll
+    for (int i = 0; i < kNext; ++i) rec[i] = a.rec[min(s + i, 2 * a.P - 1)];
+    const int4 first = rec[0];
     if (first.x < 0 || first.z != 0) continue;
-    const AwSeq q = aw_seq<true>(a, first.x);
+    const int t = first.y * kAwTile + threadIdx.x;
+    const int L = seq_len_checked(a.seq_lens, first.x, a.capacity);
+    const int64_t at = static_cast<int64_t>(first.x) * a.capacity + t;
     float acc = a.part[static_cast<int64_t>(s) * kAwTile + threadIdx.x];
+    const float before = a.prev != nullptr && t < a.capacity ? a.prev[at] : 0.f;
     int done = first.w;
-    for (int n = s + 1; done < q.R && n < 2 * a.P; ++n) {
-      const int4 r = a.rec[n];
-      if (r.x != first.x || r.y != first.y || r.z != done) continue;
+    auto add = [&](int n, const int4& r) {
+      if (done < 0 || r.x != first.x || r.y != first.y || r.z != done) return;
       acc += a.part[static_cast<int64_t>(n) * kAwTile + threadIdx.x];
       done = r.w;
-    }
-    const int t = first.y * kAwTile + threadIdx.x;
-    if (t < q.L) {
-      const int64_t at = static_cast<int64_t>(first.x) * a.capacity + t;
-      a.weights[at] = (a.prev != nullptr ? a.decay * a.prev[at] : 0.f) + acc;
-    }
+    };
+#pragma unroll
+    for (int i = 1; i < kNext; ++i)
+      if (s + i < 2 * a.P) add(s + i, rec[i]);
+    for (int n = s + kNext; done >= 0 && n < 2 * a.P; ++n) add(n, a.rec[n]);
+    if (t < L) a.weights[at] = (a.prev != nullptr ? a.decay * before : 0.f) + acc;
   }
 }
 

@@ -11,43 +11,46 @@
 // B200 mapping.  The two CTAs of a cluster run "pair" MMAs (tcgen05 cta_group::2, M = 128): CTA r
 // owns heads [64r, 64r+64) (its half of the A operand: Q for QK^T, P for PV) and each CTA's TMEM
 // receives a 64-head slice of the accumulator folded over all 128 lanes, so
-//   S tile (64 heads x 128 tokens, fp32)  = 64 TMEM columns per CTA (two buffers, and two
-//                                           partial sums over disjoint dims: 256 columns),
+//   S tile (64 heads x 128 tokens, fp32)  = 64 TMEM columns per CTA (two buffers),
 //   O      (64 heads x 512 latent, fp32)  = 256 TMEM columns per CTA.
 // Per 128-token tile the B operand of QK^T is split by tokens: CTA r holds tokens [64r, 64r+64)
 // with all 576 dims, as 9 swizzled slabs of 64 dims.  The B operand of PV is split by latent
-// columns: CTA r holds latent [256n + 128r, +128) of all 128 tokens (slabs of 32 tokens), a
-// second read of the tile's rows that hits L2 because the pair reads them within microseconds.
+// columns: CTA r holds latent [256n + 128r, +128) of all 128 tokens, a second read of the tile's
+// rows that hits L2 because the pair reads them within microseconds.
 //
-// Staging.  The TMA unit of a CTA works through its tensor copies one at a time at a roughly
-// fixed cost per copy (measured: ~0.35 us for anything from 8 KB to 72 KB from L2), so every copy
-// is large: a CTA's K rows of a tile (from HBM) come as one 3-D box of all 9 dim-slabs (72 KB),
-// and V rows (the L2 re-read) as 4-D boxes of 64 tokens x both 64-wide latent chunks x both
-// latent halves (32 KB, 2 copies per tile) into a 2-slot V ring.  Separate K and V buffers let
-// the K copy of the next tile proceed while V of the current tile waits for its softmax.
-// V rows past the segment end are zeroed in shared memory before PV (rows past a sequence's end
-// may hold anything, and 0 * NaN would poison the sum).
+// Staging.  A thread needs 0.2 us to wait for a slot, announce the bytes and issue a copy, whatever
+// its size (8 KB copies from L2: 39 GB/s per SM from one thread, 137 from four), and a slot is refilled
+// as soon as the MMAs have read it, so copies are large and K and V have a producer warp each: a CTA's K
+// rows of a tile come as two boxes (5 and 4 dim-slabs, 72 KB together) with slots of their own, V rows
+// (the L2 re-read) as 4-D boxes of 64 tokens x both 64-wide latent chunks x both latent halves (32 KB,
+// two slots, one per half tile).  Separate producers took the batch-128 call with a 2001-token window
+// from 118 to 110 us and 1024 chunk rows (window 512) from 341 to 286 us.  PV leaves out groups of 16
+// tokens with nothing to see, and rows it must not see in the other groups are zeroed in shared memory
+// before (rows past a sequence's end may hold anything, and 0 * NaN would poison the sum).
 //
-// Segments.  Every role walks the same segments of its range with a SegmentCursor.  A new
-// segment loads its sequence's Q (once both QK^T parts are done with the previous Q), restarts
-// the softmax state, overwrites O with its first PV (after the previous segment's epilogue has
-// read O and released the V ring it stages through), and ends with an epilogue that writes either
-// the final output (a segment covering its whole sequence) or an fp32 partial for the combine.
+// Segments.  Every role walks the same segments of its range with a SegmentCursor.  A new segment loads
+// its sequence's Q (once QK^T is done with the previous Q), restarts the softmax state, overwrites O with
+// its first PV (after the previous segment's epilogue has read O), and ends with an epilogue that writes
+// either the final output (a segment covering its whole sequence) or an fp32 partial for the combine.
+// The epilogue runs after the next segment's first softmax, whose P waits in registers: the wait for the
+// last PV and that softmax overlap.
 //
-// Warp roles (416 threads): warps 0-7 softmax / O correction / epilogue (two warps per TMEM lane
-// quadrant, each owning half of the S columns), warp 8 work plan and TMA producer, and in the
-// even CTA only: warps 9 and 11 QK^T, each the 16-deep K steps of its parity into its own S
-// accumulator (warp 9 also allocates TMEM in both CTAs), warps 10 and 12 PV for the two latent
-// halves.
+// Warp roles (384 threads): warps 0-7 softmax / O correction / epilogue (two warps per TMEM lane
+// quadrant, each owning half of the S columns), warp 8 work plan, then Q and K copies, warp 9 TMEM
+// allocation (both CTAs) and, in the even CTA, QK^T, warp 10 PV (even CTA), warp 11 V copies.
 //
-// FP8 cache (kFp8, 544 threads).  Rows are 576 E4M3 codes with a power-of-two scale per token (an
+// What bounds it.  At the 1.36-1.6 GHz that the power cap leaves a long call, a tile takes 2.1-2.3 us per
+// pair: 3000-3400 cycles, of which the tensor pipe works 2176 (36 x 32 for QK^T, 16 x 64 for PV); the HBM
+// floor is 1.7 us.  A call of 128 sequences of 1024..8192 tokens runs at 0.61 of the measured HBM rate.
+//
+// FP8 cache (kFp8, 640 threads).  Rows are 576 E4M3 codes with a power-of-two scale per token (an
 // E8M0 exponent byte, 2^(e - 127)): code * scale is exact in bf16, so the MMAs, the softmax and
-// the epilogue are those of the bf16 cache.  The producer copies a box's codes into the upper half
+// the epilogue are those of the bf16 cache.  The producers copy a box's codes into the upper half
 // of the bf16 buffer it will become, and the box's 64 scale bytes to the buffer's start, on a
-// CTA-local barrier; four converter warps (13-16) read both into registers, and after a barrier
-// among themselves write the exact bf16 values of code * scale over the whole buffer in the
-// swizzled layout the MMAs read (zeroing V rows past the segment end), then publish the buffer to
-// the pair barrier the MMA waits on.
+// CTA-local barrier; four converter warps for K (12-15) and four for V (16-19) write the exact bf16
+// values of code * scale over the buffer in the swizzled layout the MMAs read, then publish it to
+// the pair barrier the MMA waits on.  The conversions bound it (about 4 us a tile): 8 + 24 conversion and
+// 16 scaling instructions for 16 codes, twice per row (K and V layouts).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -68,7 +71,7 @@ constexpr int kTcKSlabsB = 4;
 static_assert(kTcKSlabsB <= kTcKSlabsA, "the QK^T issue loop is unrolled to part A's slab count");
 __host__ __device__ constexpr int tc_part_slab0(int part) { return part ? kTcKSlabsA : 0; }
 __host__ __device__ constexpr int tc_part_slabs(int part) { return part ? kTcKSlabsB : kTcKSlabsA; }
-constexpr int kTcVSlots = 2;                 // one slot per 64-token half of a tile (the PV issuer relies on it)
+constexpr int kTcVSlots = 2;                 // one slot per 64-token half of a tile (producer and PV rely on it)
 constexpr int kTcVBox = 4 * kTcSlab;         // 64 tokens x 2 chunks x 2 latent halves
 constexpr int kTcQBytes = 9 * kTcSlab;
 constexpr int kTcPBytes = 2 * kTcSlab;       // 64 heads x 128 tokens bf16, two 64-token K chunks
@@ -134,7 +137,7 @@ struct TcPlan {
 };
 
 struct TcBars {
-  uint64_t k_full[2];            // even CTA only, per QK^T part: both CTAs' K boxes landed (one arrival per CTA + tx)
+  uint64_t k_full[2];            // even CTA only, per K part: both CTAs' K boxes landed (one arrival per CTA + tx)
   uint64_t k_empty[2];           // both CTAs, per part: K box consumed by the MMAs
   uint64_t v_full[kTcVSlots];    // even CTA only: both CTAs' V box landed (one arrival per CTA + tx)
   uint64_t v_empty[kTcVSlots];   // both CTAs: V box consumed

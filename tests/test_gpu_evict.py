@@ -177,6 +177,44 @@ def test_weights_and_lengths_in_place_and_twice(m):
     assert kept[2].tolist() == list(range(17)) + [-1] * 23
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_into_fresh_pages_of_the_same_pool(m, fp8):
+    """In place with another block table: the output's pages are pages of the pool that no token uses."""
+    rng = np.random.default_rng(17)
+    lens, keep = [500, 130, 64], 100
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 18, fp8=fp8)
+    used = set(cache.table[cache.table >= 0].cpu().tolist())
+    free = [p for p in range(cache.data.shape[0] // 64) if p not in used][:6]
+    assert len(free) == 6
+    table = torch.tensor(free, dtype=torch.int32).reshape(3, 2).cuda()
+    desc = m.paged_desc(3, 2, cache.data.shape[0] // 64)
+    w = weights_like(rng, 3, cache.capacity, "heavy").cuda()
+    rows, scales = bits(cache.data), None if not fp8 else bits(cache.scales)
+    kept = torch.zeros((3, keep), dtype=torch.int32, device="cuda")
+    lens_out = torch.zeros((3,), dtype=torch.int32, device="cuda")
+    wo = torch.zeros((3, 128), device="cuda")
+    ws = torch.empty((m.evict_workspace_size(3, keep),), dtype=torch.uint8, device="cuda")
+    kw = dict(keep=keep, sinks=2, recent=20, block_table=cache.table, cache_out=cache.data, desc_out=desc,
+              block_table_out=table)
+    if fp8:
+        m.cache_evict_fp8(cache.data, cache.scales, cache.seq_lens, w, cache.desc, kept, lens_out, wo, ws,
+                          scales_out=cache.scales, **kw)
+    else:
+        m.cache_evict(cache.data, cache.seq_lens, w, cache.desc, kept, lens_out, wo, ws, **kw)
+    assert m.get_device_error() == 0
+    tab = table.cpu().numpy()
+    for b, L in enumerate(lens):
+        t = oracle.evict_keep(w[b].cpu().numpy(), L, keep, 2, 20)
+        to = tab[b][np.arange(len(t)) // 64].astype(np.int64) * 64 + np.arange(len(t)) % 64
+        frm = cache.rows_of(b, t).numpy()
+        rows[to] = rows[frm]
+        if fp8:
+            scales[to] = scales[frm]
+    assert np.array_equal(bits(cache.data), rows)
+    if fp8:
+        assert np.array_equal(bits(cache.scales), scales)
+
+
 def test_capture_replay_and_a_side_stream(m):
     rng = np.random.default_rng(8)
     cache = RowCache(m, [random_rows(rng, L) for L in (500, 200)], True, 9)

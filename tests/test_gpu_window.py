@@ -165,3 +165,52 @@ def test_bad_pages_and_lengths_are_reported(m):
     cache.seq_lens[1] = 10 ** 6    # clamped to the capacity
     call(m, cache, q.cuda(), 0, 64)
     assert m.get_device_error() & m.DEVERR_SEQLEN_RANGE
+
+
+@pytest.mark.parametrize("window,sinks", [(100, 4), (0, 0), (64, 65)])
+def test_more_rows_than_ranges(m, window, sinks):
+    """Rows by the hundred, empty ones among them: as a batch of sequences and as a chunk over one page
+    table, whose plan and combine take other ways than those of a few rows."""
+    rng = np.random.default_rng(91)
+    lens = [int(x) for x in rng.integers(0, 400, 330)]
+    lens[::17] = [0] * len(lens[::17])
+    long = random_rows(rng, 400)
+    cache = RowCache(m, [long], True, 92)
+    n = len(lens)
+    q = random_q(rng, n)
+    out, lse = (f64(x) for x in call(m, cache, q.cuda(), window, sinks, 0, torch.zeros((n,), dtype=torch.int32).cuda(),
+                                     torch.tensor(lens, dtype=torch.int32).cuda()))
+    assert m.get_device_error() == 0
+    for i in list(range(0, n, 7)) + list(range(0, n, 17)):
+        ref = oracle.window_rows(f64(q[i]), cache.values[0][:lens[i]], window, sinks, SCALE, 512)
+        assert_window_row(out[i], lse[i], ref)
+    seqs = RowCache(m, [long[:L] for L in lens[:200]], False, 93)
+    o2, l2 = (f64(x) for x in call(m, seqs, q[:200].cuda(), window, sinks))
+    assert m.get_device_error() == 0
+    for i in range(0, 200, 9):
+        assert_window_row(o2[i], l2[i], oracle.window_rows(f64(q[i]), seqs.values[i], window, sinks, SCALE, 512))
+
+
+@pytest.mark.parametrize("lens", [[0], [100], [0, 64], [64, 0], [0, 0]])
+def test_calls_of_one_range(m, lens):
+    """The smallest calls have one work range and no combine: empty rows beside short ones, and a forced one."""
+    rng = np.random.default_rng(95)
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 96, max_len=64 if len(lens) == 2 else 128)
+    q = random_q(rng, len(lens))
+    for splits in (0, 1):
+        out, lse = (f64(x) for x in call(m, cache, q.cuda(), 40, 3, splits))
+        assert m.get_device_error() == 0
+        for b, L in enumerate(lens):
+            assert_window_row(out[b], lse[b], oracle.window_rows(f64(q[b]), cache.values[b], 40, 3, SCALE, 512))
+
+
+def test_many_ranges_per_row(m):
+    """One row over more ranges than the combine reads at a time, alone and beside others."""
+    rng = np.random.default_rng(97)
+    for lens, splits in (([12000], 60), ([9000, 100, 6000], 100), ([5000] * 12, 90)):
+        cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 98)
+        q = random_q(rng, len(lens))
+        out, lse = (f64(x) for x in call(m, cache, q.cuda(), 11000, 40, splits))
+        assert m.get_device_error() == 0
+        for b in range(0, len(lens), 2):
+            assert_window_row(out[b], lse[b], oracle.window_rows(f64(q[b]), cache.values[b], 11000, 40, SCALE, 512))
