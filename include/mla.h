@@ -3,7 +3,9 @@
  * decode over the compressed latent KV cache, in its weight-absorbed form: (1) cache append,
  * (2) query absorption, (3) decode attention (split over work ranges, merged by a combine),
  * (4) value un-absorption, and beside them (1') the down-projection + append of new tokens,
- * (6) the output projection and (7) chunked-prefill attention.
+ * (6) the output projection and (7) chunked-prefill attention.  For a cache that is kept bounded:
+ * (3-window) attention with a sliding window and sinks, (8) attention weights accumulated per cached
+ * token, (9) eviction by those weights and (1-at) the append into a shortened cache.
  *
  * Sources (page title, section):
  *   [DR] 《DeepSeek-V2》深度解读报告 — §2.2 Low-Rank Key-Value Joint Compression,
@@ -198,9 +200,10 @@ int32_t mla_decode_num_splits(int32_t batch, int32_t max_seq_len, int32_t num_sp
 
 /*
  * Bytes of workspace mla_decode_attn needs, with P = mla_decode_num_splits(batch, max_seq_len,
- * num_splits): range partials O [2P, 128, 512] fp32 and (m, l) [2P, 128] fp32 each, then the
- * plan table [batch + 2] int32 (per sequence its cost-line offset or first range, the total, the
- * plan kind; rounded up to 16 bytes).
+ * num_splits): range partials O [2P, 128, 512] fp32 and (m, l) [2P, 128] fp32 each, the split rows
+ * [P] int32 (the row that a range begins and another one continues), then the plan table [batch + 2]
+ * int32 (per sequence its cost-line offset or first range, the total, the plan kind); together
+ * rounded up to 16 bytes.
  */
 size_t mla_decode_workspace_size(int32_t batch, int32_t max_seq_len, int32_t num_splits);
 

@@ -5,11 +5,14 @@
 // below every number); L <= keep keeps all.  The kept tokens' rows move, in order, to slots
 // 0 .. n - 1 of the same cache or of another one.
 //
-// Two kernels.  The selection finds the k-th largest weight by its bits (a radix select: four 8-bit
-// digits from the top, each one histogram of the keys that share the digits found so far), then
-// numbers the kept tokens in order.  A cluster of CTAs shares a sequence: each holds the order keys
-// of its slice in shared memory, and the histograms are summed through distributed shared memory.
-// The move is a copy bound by HBM: the rows' bytes read once and written once.
+// The selection finds the k-th largest weight by its bits (a radix select: 8-bit digits from the top, each one
+// histogram of the keys that share the digits found so far, done early when all of them are kept), then
+// numbers the kept tokens in order.  A cluster of CTAs shares a long sequence: each holds the order keys of
+// its slice in shared memory, and the histograms are summed through distributed shared memory.  It is bound
+// by the latency of its steps: 3-6 us beside the launch for up to 8192 tokens a CTA.
+//
+// The move is a copy bound by HBM, the rows' bytes read once and written once: 128 x 1024 rows (302 MB) in
+// 53 us, 5.7 TB/s, 0.88 of the measured copy rate.  Few rows are moved by the selection kernel itself.
 #pragma once
 
 #include "append.cuh"
@@ -63,10 +66,81 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
   return v;
 }
 
-// grid = batch * C CTAs in clusters of C: cluster b selects for sequence b.
+// A cache of rows of `row_bytes` bytes (1152 bf16, 576 FP8) with, for FP8, a scale byte per row.
+struct EvictCache {
+  CacheView v;
+  uint8_t* rows;
+  uint8_t* scales;
+};
+
+// What the move writes beside the rows: the weights at their new slots, zeros in the slots that the
+// eviction freed (up to the old length), and the new lengths.
+// me of all threads.
+__device__ __forceinline__ void ev_write_weights(const EvictWorkspace& ws, int b, int L, int keep, int capacity_out,
+                                                 float* weights_out, int32_t* lens_out, int64_t me, int64_t all) {
+  const int n = min(L, keep);
+  float* wo = weights_out + static_cast<int64_t>(b) * capacity_out;
+  const float* kw = ws.w + static_cast<int64_t>(b) * keep;
+  for (int64_t j = me; j < min(L, capacity_out); j += all) wo[j] = j < n ? kw[j] : 0.f;
+  if (me == 0) lens_out[b] = n;
+}
+
+// What a selection that also moves the rows needs for it.
+struct EvictMove {
+  EvictCache src, dst;
+  int capacity_out;
+  float* weights_out;
+  int32_t* lens_out;
+};
+// At most this many kept tokens are moved by the selection itself (one CTA of the cluster does it): one launch
+// instead of two, which is what a short call costs.  300 tokens to 128: 10.2 us a call instead of 12.1, 128 x
+// 1000..4000 to 64: 12.2 instead of 14.7.  Its reads are all in flight at once; more rows are better spread
+// over the device by a launch of their own.
+constexpr int kEvMoveRows = 128;
+
+// One CTA moves the first n <= kEvMoveRows slots' rows of sequence b: reads them all, waits for all threads,
+// writes them (in place whatever a write overwrites belongs to an evicted token or has been read).
+template <int kRowBytes>
+__device__ void ev_move_rows(const EvictMove& mv, int b, int n, const int32_t* kp, int64_t* rows) {
+  constexpr int kPieces = kRowBytes / 16, kPer = kEvMoveRows * kPieces / kEvThreads;
+  static_assert(kEvMoveRows * kPieces % kEvThreads == 0, "every thread moves as many pieces");
+  if (threadIdx.x < kEvMoveRows) {
+    const int j = threadIdx.x;
+    int64_t s = -1, d = -1;
+    if (j < n) {
+      s = cache_row(mv.src.v, b, kp[j]);
+      d = cache_row(mv.dst.v, b, j);
+      if (s < 0 || d < 0) s = d = -1;
+    }
+    rows[j] = s;
+    rows[kEvMoveRows + j] = d;
+  }
+  __syncthreads();
+  uint4 x[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = u * kEvThreads + threadIdx.x, r = i / kPieces;
+    if (rows[r] >= 0) x[u] = reinterpret_cast<const uint4*>(mv.src.rows + rows[r] * kRowBytes)[i - r * kPieces];
+  }
+  uint8_t sc = 0;
+  const bool scale = threadIdx.x < kEvMoveRows && mv.src.scales != nullptr && rows[threadIdx.x] >= 0;
+  if (scale) sc = mv.src.scales[rows[threadIdx.x]];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = u * kEvThreads + threadIdx.x, r = i / kPieces;
+    if (rows[r] >= 0)
+      reinterpret_cast<uint4*>(mv.dst.rows + rows[kEvMoveRows + r] * kRowBytes)[i - r * kPieces] = x[u];
+  }
+  if (scale) mv.dst.scales[rows[kEvMoveRows + threadIdx.x]] = sc;
+}
+
+// grid = batch * C CTAs in clusters of C: cluster b selects for sequence b, and (kRowBytes > 0) moves its rows.
+template <int kRowBytes>
 __global__ void __launch_bounds__(kEvThreads, 1)
-    evict_select_kernel(const float* __restrict__ weights, const int32_t* __restrict__ seq_lens, int capacity, int keep,
-                        int sinks, int recent, int C, int32_t* __restrict__ kept, EvictWorkspace ws) {
+    evict_select_kernel(const float* weights, const int32_t* seq_lens, int capacity, int keep,
+                        int sinks, int recent, int C, int32_t* kept, EvictWorkspace ws,
+                        const __grid_constant__ EvictMove mv) {
   extern __shared__ __align__(16) uint8_t ev_raw[];
   EvSmem& sm = *reinterpret_cast<EvSmem*>(ev_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -84,11 +158,21 @@ __global__ void __launch_bounds__(kEvThreads, 1)
   int32_t* kp = kept + static_cast<int64_t>(b) * keep;
   float* kw = ws.w + static_cast<int64_t>(b) * keep;
   const int me = rank * kEvThreads + tid, all = C * kEvThreads;
-  if (L <= keep) {   // the same in every CTA of the cluster: none of them reaches a cluster barrier
+  // Every thread comes here once the kept tokens are written: rank 0 moves the rows, all write the weights.
+  auto finish = [&]() {
+    if constexpr (kRowBytes > 0) {
+      if (C > 1) cluster_sync();
+      else __syncthreads();
+      ev_write_weights(ws, b, L, keep, mv.capacity_out, mv.weights_out, mv.lens_out, me, all);
+      if (rank == 0) ev_move_rows<kRowBytes>(mv, b, min(L, keep), kp, reinterpret_cast<int64_t*>(sm.hist));
+    }
+  };
+  if (L <= keep) {   // the same in every CTA of the cluster
     for (int j = me; j < keep; j += all) {
       kp[j] = j < L ? j : -1;
       kw[j] = j < L ? w[j] : 0.f;
     }
+    finish();
     return;
   }
   auto write_sure = [&](int from, int step) {   // the tokens that are kept whatever they weigh
@@ -101,6 +185,7 @@ __global__ void __launch_bounds__(kEvThreads, 1)
   const int k = keep - sinks - recent;
   if (k == 0) {
     write_sure(me, all);
+    finish();
     return;
   }
   // This CTA's slice of the middle, in order: tokens first + [0, n).
@@ -261,27 +346,8 @@ __global__ void __launch_bounds__(kEvThreads, 1)
       e0 += __popc(be);
     }
   }
+  finish();
   if (C > 1) cluster_sync();   // no CTA leaves while another reads its counts
-}
-
-// A cache of rows of `row_bytes` bytes (1152 bf16, 576 FP8) with, for FP8, a scale byte per row.
-struct EvictCache {
-  CacheView v;
-  uint8_t* rows;
-  uint8_t* scales;
-};
-
-// What the move writes beside the rows: the weights at their new slots, zeros in the slots that the
-// eviction freed (up to the old length), and the new lengths.
-__device__ __forceinline__ void ev_write_weights(const EvictWorkspace& ws, int b, int L, int keep, int capacity_out,
-                                                 float* weights_out, int32_t* lens_out) {
-  const int n = min(L, keep);
-  float* wo = weights_out + static_cast<int64_t>(b) * capacity_out;
-  const float* kw = ws.w + static_cast<int64_t>(b) * keep;
-  for (int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; j < min(L, capacity_out);
-       j += static_cast<int64_t>(gridDim.x) * blockDim.x)
-    wo[j] = j < n ? kw[j] : 0.f;
-  if (blockIdx.x == 0 && threadIdx.x == 0) lens_out[b] = n;
 }
 
 // Move into another buffer: grid = (blocks of kEvRows slots, batch).  Every row on its own, so the
@@ -326,7 +392,9 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(EvictCache src, EvictCa
     const int r = i / kPieces;
     if (r < kEvRows && from[r] >= 0) reinterpret_cast<uint4*>(dst.rows + to[r] * kRowBytes)[i - r * kPieces] = x[u];
   }
-  ev_write_weights(ws, b, L, keep, capacity_out, weights_out, lens_out);
+  ev_write_weights(ws, b, L, keep, capacity_out, weights_out, lens_out,
+                   static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                   static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 // Move within one buffer: grid = (9 column slices, batch).  A kept token never moves to a later slot,
@@ -380,7 +448,9 @@ __global__ void __launch_bounds__(256) evict_compact_kernel(EvictCache src, Evic
     if (scale) dst.scales[to[tid]] = sc;
     __syncthreads();   // from and to are read above
   }
-  ev_write_weights(ws, b, L, keep, capacity_out, weights_out, lens_out);
+  ev_write_weights(ws, b, L, keep, capacity_out, weights_out, lens_out,
+                   static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                   static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 }  // namespace mla

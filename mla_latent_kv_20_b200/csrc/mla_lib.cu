@@ -750,15 +750,19 @@ mla_status launch_evict(const void* cache, const uint8_t* scales, const int32_t*
   int C = 1;
   while (C < mla::kEvMaxCluster && capacity / C > 4096 && 2 * C * batch <= device_sm_count()) C *= 2;
   const mla::EvictWorkspace ws = mla::ev_carve(workspace, batch, keep);
-  if (cudaFuncSetAttribute(mla::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const mla::EvictCache src{v, static_cast<uint8_t*>(const_cast<void*>(cache)), const_cast<uint8_t*>(scales)};
+  const mla::EvictCache dst{vo, static_cast<uint8_t*>(cache_out), scales_out};
+  const bool moved = keep <= mla::kEvMoveRows;   // by the selection itself
+  auto select = !moved ? mla::evict_select_kernel<0>
+                       : (fp8 ? mla::evict_select_kernel<mla::kDRow> : mla::evict_select_kernel<2 * mla::kDRow>);
+  if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(sizeof(mla::EvSmem))) != cudaSuccess)
     return MLA_ERR_CUDA;
   cudaStream_t s = as_stream(stream);
-  st = launch_clusters(mla::evict_select_kernel, dim3(batch * C), dim3(mla::kEvThreads), C, sizeof(mla::EvSmem), s,
-                       weights, seq_lens, capacity, keep, sinks, recent, C, kept, ws);
-  if (st != MLA_OK) return st;
-  const mla::EvictCache src{v, static_cast<uint8_t*>(const_cast<void*>(cache)), const_cast<uint8_t*>(scales)};
-  const mla::EvictCache dst{vo, static_cast<uint8_t*>(cache_out), scales_out};
+  st = launch_clusters(select, dim3(batch * C), dim3(mla::kEvThreads), C, sizeof(mla::EvSmem), s, weights, seq_lens,
+                       capacity, keep, sinks, recent, C, kept, ws,
+                       mla::EvictMove{src, dst, capacity_out, weights_out, lens_out});
+  if (st != MLA_OK || moved) return st;
   if (in_place)
     return launch_chained(fp8 ? mla::evict_compact_kernel<mla::kDRow> : mla::evict_compact_kernel<2 * mla::kDRow>,
                           dim3(9, batch), dim3(256), 0, s, src, dst, static_cast<const int32_t*>(kept), ws, keep,
