@@ -314,12 +314,12 @@ TRAFFIC_SOURCES = ("csrc/decode_tc.cuh", "csrc/decode_common.cuh", "csrc/ptx.cuh
                    "csrc/decode_launch.cuh")
 MEASURED_TRAFFIC = {   # workload[@ranges] -> {"bytes": int, "sha256": str, "profile": str}
     "b128_u1024_8192_paged": {
-        "bytes": 692713728 + 27520512 + 36337664,
-        "sha256": "8a3f5dfa12b42f6720b1337f7e46a5337e6e4a9823a12bd11a065ea0c4e23e0d",
+        "bytes": 692425216 + 26957312 + 36340224,
+        "sha256": "374ac24a269fb544c5c84ba96d2e0fac46ddf38071dc001c9f3cd7304fd70184",
         "profile": "profiles/decode_tc_b128_u1024_8192_paged.md (decode + combine, ncu cache flush per kernel)"},
     "b32_l4096": {
-        "bytes": 155804416 + 3546368 + 16862976,
-        "sha256": "8a3f5dfa12b42f6720b1337f7e46a5337e6e4a9823a12bd11a065ea0c4e23e0d",
+        "bytes": 155795456 + 3212032 + 16864512,
+        "sha256": "374ac24a269fb544c5c84ba96d2e0fac46ddf38071dc001c9f3cd7304fd70184",
         "profile": "profiles/decode_tc_b32_l4096.md (decode + combine, ncu cache flush per kernel)"},
 }
 

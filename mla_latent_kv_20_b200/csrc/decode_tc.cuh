@@ -207,11 +207,8 @@ __device__ __forceinline__ void tma_load_4d_local(void* dst, const CUtensorMap* 
       : "memory");
 }
 
-// ------------------------------------------------------------------------------ TMA producer
-// One warp.  Lane 0 issues the copies, in the order K(0), K(1), V(0), K(2), V(1), ..., V(n-1):
-// K one tile ahead, so QK^T of tile i+1 never waits behind V of tile i.  (Pulling later K tiles
-// into L2 ahead of their copies with plain prefetches measured no faster and adds code to the
-// per-tile loop, so the K copies read HBM directly.)
+// ------------------------------------------------------------------------------ TMA producers
+// Two warps, one lane of each issuing: one copies Q and K, one V, each as soon as its slots are free.
 //  K(i): CTA r's 64 tokens [tile0 + 64r, +64) x 576 dims as two boxes, one per QK^T part
 //        (5 and 4 dim-slabs).  A half-tile past the split end is loaded from a negative row
 //        (zeros); its scores are masked anyway.
@@ -692,13 +689,10 @@ __device__ __forceinline__ void store_rows_64b(uint8_t* stage, const uint32_t* w
 // L2 prefetch of the K rows the producer will copy kTcPfDist tiles later.  A K copy is issued only
 // once QK^T has released the slot it refills (a single K slot per part), so its HBM latency sits
 // on the critical loop; with the rows already in L2 it shrinks to the L2 latency.  The softmax
-// warps issue the prefetches (plain prefetch.global.L2, not the TMA unit, which serialises its
-// copies): this CTA's 64 rows of the tile are one contiguous 72 KB run, 576 lines over 256
-// threads, once per tile.  Contiguous caches only: with pages at permuted addresses the
-// prefetches measured slower (b32 x 4096 paged 65.6 -> 66.6 us, 128 mixed lengths paged 219 ->
-// 223 us), against 61.8 -> 58.6 and 200 -> 195 us for the same batches contiguous; and slower
-// still with the page rows handed over by the producer from its block-id window, so that no
-// thread waits for the block table (212 -> 225 us for the batch-128 paged workload).
+// warps issue the prefetches: this CTA's 64 rows of the tile are one contiguous 72 KB run, 576 lines
+// over 256 threads, once per tile.  Contiguous caches only.  (Bulk prefetches by the K producer, for
+// both layouts: 74 x 2048 in pages 55.5 -> 53.8 us, but 4 x 131072 contiguous 158 -> 166 us and 128 mixed
+// lengths in pages 194 -> 200 us.)
 constexpr int kTcPfDist = 2;
 template <bool kMapped, class Map>
 __device__ __forceinline__ void tc_prefetch_tile(const DecodeTcArgs& a, const Map& map, int b, int tok0, int t_end) {
