@@ -51,7 +51,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 //   O      [2P][128][512] fp32   (unnormalised partial sums of c)
 //   m      [2P][128]      fp32   (running max, log2 domain)
 //   l      [2P][128]      fp32   (running sum of exp2(s - m))
-//   split  [P]            int32  (the row whose first piece range p holds if that row is split, else -1)
 //   plan   [batch + 2]    int32  (balanced: cost prefix W_b of each sequence, [batch] = C;
 //                                 per sequence: first range of each sequence, [batch] = ranges used;
 //                                 [batch + 1] = the plan kind)
@@ -59,7 +58,6 @@ struct Workspace {
   float* o;
   float* m;
   float* l;
-  int32_t* split;
   int32_t* off;
 };
 __host__ __device__ __forceinline__ Workspace ws_carve(void* base, int P) {
@@ -67,13 +65,12 @@ __host__ __device__ __forceinline__ Workspace ws_carve(void* base, int P) {
   w.o = reinterpret_cast<float*>(base);
   w.m = w.o + static_cast<int64_t>(2 * P) * kHeads * kDLat;
   w.l = w.m + static_cast<int64_t>(2 * P) * kHeads;
-  w.split = reinterpret_cast<int32_t*>(w.l + static_cast<int64_t>(2 * P) * kHeads);
-  w.off = w.split + P;
+  w.off = reinterpret_cast<int32_t*>(w.l + static_cast<int64_t>(2 * P) * kHeads);
   return w;
 }
 __host__ __device__ __forceinline__ size_t ws_bytes(int batch, int P) {
   const size_t partials = static_cast<size_t>(2 * P) * kHeads * (kDLat + 2) * sizeof(float);
-  return partials + ((static_cast<size_t>(batch) + 2 + P) * sizeof(int32_t) + 15) / 16 * 16;
+  return partials + ((static_cast<size_t>(batch) + 2) * sizeof(int32_t) + 15) / 16 * 16;
 }
 
 // Effective length of sequence b: seq_lens[b] clamped to [0, capacity] (error word set if it
@@ -207,8 +204,8 @@ struct SegmentCursor {
 // Combine: merges the partials of split rows and writes the empty ones (out_lat = 0, lse = -inf).
 //   out = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p,   M = max_p m_p,   in ascending range order.
 // kByRange: block x < P takes the row whose first piece range x holds, if it is split (fewer rows are split
-// than there are ranges), and the blocks from P on look over 32 rows each for empty ones; otherwise block
-// x takes row x.  A warp covers 128 kCols latent columns of a head (a lane kCols pieces of four), a block
+// than there are ranges), looked up in the plan table, and the blocks from P on look over 32 rows each
+// for empty ones; otherwise block x takes row x.  A warp covers 128 kCols latent columns of a head (a lane kCols pieces of four), a block
 // of four warps kCols heads: kCols = 4 where there are rows enough to fill the device, 1 where few rows
 // may have many partials each.  8 / kCols partials are in flight at a time; their m and l are read by
 // lane i for the row's i-th range, 32 ranges at once.
@@ -237,22 +234,31 @@ __global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int P, int B
       for (; empty != 0; empty &= empty - 1) write_empty(b0 + __ffs(empty) - 1);
       return;
     }
-    p0 = blockIdx.x;
-    b = ws.split[p0];
-    if (b < 0) return;
+    // The last row that starts at or before the key: range p itself, or the cost at which it ends.  (A row
+    // that begins there or later has no piece in it.)  32 probes a round.
+    const int key = per_seq ? static_cast<int>(blockIdx.x) : muldiv(static_cast<int>(blockIdx.x) + 1, C, P) - 1;
+    if (key < 0) return;   // ends where the line of tiles begins: no piece
+    int lo = 0, n = B;     // off[lo] <= key: among rows [lo, lo + n)
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const bool le = lane * step < n && ws.off[lo + lane * step] <= key;
+      const int last = __popc(__ballot_sync(0xffffffffu, le)) - 1;   // the offsets ascend
+      lo += last * step;
+      n = min(step, n - last * step);
+    }
+    b = lo;
   }
   // Ranges [p0, p1] hold b's pieces; in the per-sequence plan each holds one (slot 2p).  In the balanced
   // plan they are those that hold its first and last tiles, at costs off + kSegCost and off + span - 1;
   // a piece is the range's last segment (slot 2p + 1) where the range began before b, x_p < W_b = off,
   // and a range with x_p = x_{p+1} is empty.
   const int off = ws.off[b], span = ws.off[b + 1] - off;
-  if (!kByRange) {
-    if (span == 0) {
-      if (blockIdx.y == 0) write_empty(b);
-      return;
-    }
-    p0 = per_seq ? off : range_of_cost(off + kSegCost, P, C);
+  if (span == 0) {
+    if (!kByRange && blockIdx.y == 0) write_empty(b);
+    return;
   }
+  p0 = per_seq ? off : range_of_cost(off + kSegCost, P, C);
+  if (kByRange && p0 != blockIdx.x) return;
   const int p1 = per_seq ? off + span - 1 : range_of_cost(off + span - 1, P, C);
   if (p0 == p1) return;   // finished by the decode kernel
   const int h = blockIdx.y * kCols + (kCols == 4 ? warp : 0);

@@ -839,7 +839,6 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       }
     }
   };
-  int split_row = -1;   // the split row whose first piece this range holds (at most one), for the combine
   bool more = cur.next(a.seq_lens, a.capacity, rows, sg);
   while (more) {
   const auto map = rows.map(sg.len);
@@ -988,12 +987,10 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   done.direct = sg.direct;
   done.m = m_used;
   done.l = l_run;
-  if (!sg.direct && sg.tok_begin == 0) split_row = sg.b;
   ++k;
   more = cur.next(a.seq_lens, a.capacity, rows, sg);
   }
   if (ok && k > 0) epilogue(k - 1, red + (g & 1) * 256);   // the buffer the last tile did not use
-  if (rank == 0 && threadIdx.x == 0) a.ws.split[pair] = split_row;
 }
 
 // A call of one range has no split rows and is not followed by a combine: its empty rows are written here.
@@ -1285,8 +1282,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < kTcSoftmaxWarps && a.P == 1) tc_empty_rows<Rows>(a, rank);
-  if (!busy) {   // an idle range: only the teardown below
-    if (rank == 0 && threadIdx.x == 0) a.ws.split[pair] = -1;
+  if (!busy) {
+    // an idle range: only the teardown below
   } else if (warp < kTcSoftmaxWarps) {
     tc_softmax<kMapped, Rows>(a, pl, pair, smem, bars, red, tmem, rank, abort_flag);
   } else if (warp == kTcProducerWarp || warp == kTcVProducerWarp) {

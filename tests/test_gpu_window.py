@@ -214,3 +214,20 @@ def test_many_ranges_per_row(m):
         assert m.get_device_error() == 0
         for b in range(0, len(lens), 2):
             assert_window_row(out[b], lse[b], oracle.window_rows(f64(q[b]), cache.values[b], 11000, 40, SCALE, 512))
+
+
+@pytest.mark.parametrize("filled", [0, 1, 2, 40])
+def test_many_rows_almost_all_empty(m, filled):
+    """More rows than ranges, but fewer tiles than ranges."""
+    rng = np.random.default_rng(99)
+    cache = RowCache(m, [random_rows(rng, 700)], True, 100)
+    n = 200
+    lens = np.zeros(n, np.int32)
+    lens[rng.choice(n, filled, replace=False)] = 600 if filled < 40 else 130
+    q = random_q(rng, n)
+    out, lse = (f64(x) for x in call(m, cache, q.cuda(), 500, 4, 0, torch.zeros((n,), dtype=torch.int32).cuda(),
+                                     torch.from_numpy(lens).cuda()))
+    assert m.get_device_error() == 0
+    for i in range(n):
+        if lens[i] or i % 9 == 0:
+            assert_window_row(out[i], lse[i], oracle.window_rows(f64(q[i]), cache.values[0][:lens[i]], 500, 4, SCALE, 512))
