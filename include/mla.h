@@ -340,8 +340,9 @@ mla_status mla_prefill_attn_weights(const mla_bf16* q_full, const mla_bf16* cach
  *   weights_out[b * capacity_out + j] = the weight of t_j for j < n, 0 for n <= j < min(L, capacity_out)
  *   lens_out[b]                       = n
  * and nothing else: rows and weights behind these are left as they were.
- *   keep >= 1, sinks >= 0, recent >= 0, sinks + recent <= keep <= capacity_out, batch <= num_seqs of both
- *   descriptors (MLA_ERR_INVALID_ARG otherwise), batch <= 16384 (MLA_ERR_UNSUPPORTED)
+ *   keep >= 1, sinks >= 0, recent >= 0, sinks + recent <= keep, min(keep, capacity) <= capacity_out,
+ *   batch <= num_seqs of both descriptors (MLA_ERR_INVALID_ARG otherwise), batch <= 16384
+ *   (MLA_ERR_UNSUPPORTED)
  *   seq_lens [batch] int32   weights [batch, capacity] fp32   kept [batch, keep] int32
  *   lens_out [batch] int32   weights_out [batch, capacity_out] fp32
  *   workspace >= mla_evict_workspace_size(batch, keep) bytes, 16-byte aligned

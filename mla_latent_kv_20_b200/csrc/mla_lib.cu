@@ -729,7 +729,7 @@ mla_status launch_evict(const void* cache, const uint8_t* scales, const int32_t*
   if (st == MLA_OK) st = check_cache(desc_out, cache_out, block_table_out, &vo);
   if (st != MLA_OK) return st;
   const int capacity = cache_capacity(desc), capacity_out = cache_capacity(desc_out);
-  if (keep > capacity_out) return MLA_ERR_INVALID_ARG;
+  if (std::min(keep, capacity) > capacity_out) return MLA_ERR_INVALID_ARG;   // what a sequence may keep has to fit
   if (batch > desc.num_seqs || batch > desc_out.num_seqs) return MLA_ERR_INVALID_ARG;
   // The same buffer in the same layout, or two that do not meet.
   const bool in_place = cache_out == cache;

@@ -119,6 +119,9 @@ def test_ties_and_special_weights(m, in_place, kind):
 @pytest.mark.parametrize("in_place", [False, True])
 def test_everything_fits(m, in_place):
     check(m, [5, 0, 64, 130], True, False, in_place, "heavy", 256, 4, 4, 5, max_len=512)
+    check(m, [5, 0, 64, 130], True, False, in_place, "heavy", 1000, 4, 4, 6)   # more than a sequence can hold
+    check(m, [5, 130], False, True, in_place, "heavy", 1000, 400, 4, 7)
+    check(m, [5, 100], False, False, in_place, "heavy", 128, 0, 4, 8)
 
 
 def test_between_layouts(m):
