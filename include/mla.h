@@ -341,8 +341,8 @@ mla_status mla_prefill_attn_weights(const mla_bf16* q_full, const mla_bf16* cach
  *   lens_out[b]                       = n
  * and nothing else: rows and weights behind these are left as they were.
  *   keep >= 1, sinks >= 0, recent >= 0, sinks + recent <= keep, min(keep, capacity) <= capacity_out,
- *   batch <= num_seqs of both descriptors (MLA_ERR_INVALID_ARG otherwise), batch <= 16384
- *   (MLA_ERR_UNSUPPORTED)
+ *   batch <= num_seqs of both descriptors (MLA_ERR_INVALID_ARG otherwise), batch <= 16384,
+ *   keep <= 2^30 (MLA_ERR_UNSUPPORTED)
  *   seq_lens [batch] int32   weights [batch, capacity] fp32   kept [batch, keep] int32
  *   lens_out [batch] int32   weights_out [batch, capacity_out] fp32
  *   workspace >= mla_evict_workspace_size(batch, keep) bytes, 16-byte aligned

@@ -723,7 +723,8 @@ mla_status launch_evict(const void* cache, const uint8_t* scales, const int32_t*
   const int row_bytes = fp8 ? mla::kDRow : 2 * mla::kDRow;
   if (batch < 0 || keep < 1 || sinks < 0 || recent < 0) return MLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(sinks) + recent > keep) return MLA_ERR_INVALID_ARG;
-  if (batch > mla::kMaxDecodeBatch) return MLA_ERR_UNSUPPORTED;
+  // (the kernels count slots in 32 bits, a grid's threads beyond the last)
+  if (batch > mla::kMaxDecodeBatch || keep > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   CacheView v, vo;
   mla_status st = check_cache(desc, cache, block_table, &v);
   if (st == MLA_OK) st = check_cache(desc_out, cache_out, block_table_out, &vo);

@@ -28,6 +28,8 @@ def test_evict_refusals(host_only):  # noqa: F811
     assert call(keep=2049, nbytes=1 << 40, desc_out=m.contiguous_desc(8, 2048)) == 1
     assert call(keep=9000, nbytes=1 << 40, desc_out=m.contiguous_desc(8, 4095)) == 1
     assert call(batch=0, keep=9000) == 0      # more than a sequence can hold: nothing is ever evicted
+    assert call(batch=0, keep=1 << 30) == 0 and call(batch=0, keep=(1 << 30) + 1) == 2
+    assert call(keep=2 ** 31 - 1, nbytes=1 << 62) == 2
     assert call(desc_out=m.contiguous_desc(7, 4096)) == 1
     for name in ("lens", "weights", "kept", "lens_out", "weights_out", "cache", "out"):
         assert call(**{name: None}) == 1, name
