@@ -314,12 +314,12 @@ TRAFFIC_SOURCES = ("csrc/decode_tc.cuh", "csrc/decode_common.cuh", "csrc/ptx.cuh
                    "csrc/decode_launch.cuh")
 MEASURED_TRAFFIC = {   # workload[@ranges] -> {"bytes": int, "sha256": str, "profile": str}
     "b128_u1024_8192_paged": {
-        "bytes": 692425216 + 26957312 + 36340224,
-        "sha256": "374ac24a269fb544c5c84ba96d2e0fac46ddf38071dc001c9f3cd7304fd70184",
+        "bytes": 692623104 + 26407936 + 36341760,
+        "sha256": "f0be339353ea62562caede51eaad06f770b741a5f5abb3a6c390f7a56b4faf70",
         "profile": "profiles/decode_tc_b128_u1024_8192_paged.md (decode + combine, ncu cache flush per kernel)"},
     "b32_l4096": {
-        "bytes": 155795456 + 3212032 + 16864512,
-        "sha256": "374ac24a269fb544c5c84ba96d2e0fac46ddf38071dc001c9f3cd7304fd70184",
+        "bytes": 155803648 + 3008256 + 16865280,
+        "sha256": "f0be339353ea62562caede51eaad06f770b741a5f5abb3a6c390f7a56b4faf70",
         "profile": "profiles/decode_tc_b32_l4096.md (decode + combine, ncu cache flush per kernel)"},
 }
 
