@@ -24,8 +24,10 @@
 // What bounds it.  A decode step: HBM.  128 sequences of 1024..8192 tokens in pages (670 MB, none of it in L2)
 // take 127 us, 5.3 TB/s, 0.82 of the measured copy rate; of these about 7 us go before the first tile's
 // scores.  A chunk: the tensor pipe; 64 rows of 74 tiles take 113 us, 2620 cycles a unit against the 2304
-// of its 36 MMAs.  FP8: the converters and the slots' round trip (copy, conversion, MMAs, then the next copy,
-// 5500 cycles a unit): 74 x 4096, 59 us.
+// of its 36 MMAs.  FP8: the bandwidth of shared memory, which the
+// MMAs' operands (2304 cycles a unit), the codes' way in and out (1152) and the bf16 values written (1152)
+// share: 5500 cycles a unit, 74 x 4096 in 59 us.  (Codes in two buffers of their own, refilled during the
+// conversion: 64; sixteen converter warps: 29.0 -> 30.0 for 32 x 4096.)
 //
 // Split.  The units of all sequences (sequence, then tile, then row) are laid end to end and cut into P
 // equal ranges, one per CTA pair.  A tile whose rows fall into several ranges leaves partial sums in the
@@ -376,7 +378,7 @@ __device__ bool aw_convert(const AwArgs& a, const AwPlan& plan, uint8_t* smem, A
         const int i = ct + k * kAwConvThreads;
         const int row = (i >> 2) & 7, pc = i & 3;
         uint4 lo, hi;
-        e4m3x16_to_bf16(c[k], 1.f, lo, hi);
+        e4m3x16_to_bf16<false>(c[k], __nv_bfloat162(), lo, hi);
         uint8_t* dst = buf + (i >> 5) * 1024 + row * 128;
         *reinterpret_cast<uint4*>(dst + (((2 * pc) ^ row) << 4)) = lo;
         *reinterpret_cast<uint4*>(dst + (((2 * pc + 1) ^ row) << 4)) = hi;

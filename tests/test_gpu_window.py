@@ -231,3 +231,18 @@ def test_many_rows_almost_all_empty(m, filled):
     for i in range(n):
         if lens[i] or i % 9 == 0:
             assert_window_row(out[i], lse[i], oracle.window_rows(f64(q[i]), cache.values[0][:lens[i]], 500, 4, SCALE, 512))
+
+
+@pytest.mark.parametrize("window", [1 << 30, 200])
+def test_fp8_rows_of_any_scale_have_the_bits_of_their_bf16_values(m, window):
+    """Row scales from 2^-127 (values below bf16's normal range, rounded to it once) to 2^118."""
+    rng = np.random.default_rng(91)
+    exps, L = [-120, -119, -100, -7, 0, 7, 60, 124], 300
+    seqs = [torch.from_numpy(rng.standard_normal((L, 576)) * 2.0 ** k).to(torch.bfloat16) for k in exps]
+    coded = RowCache(m, seqs, True, 92, fp8=True)
+    plain = RowCache(m, [torch.from_numpy(v).to(torch.bfloat16) for v in coded.values], True, 92)
+    assert int(coded.scales.min()) == 0 and int(coded.scales.max()) > 240
+    q = torch.stack([(r.double() * 2.0 ** -k).to(torch.bfloat16) for r, k in zip(random_q(rng, len(exps)), exps)]).cuda()
+    a, b = call(m, coded, q, window, 4), call(m, plain, q, window, 4)
+    assert torch.isfinite(a[1]).all() and (a[0] != 0).any(dim=2).all()
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
