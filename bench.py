@@ -314,12 +314,12 @@ TRAFFIC_SOURCES = ("csrc/decode_tc.cuh", "csrc/decode_common.cuh", "csrc/ptx.cuh
                    "csrc/decode_launch.cuh")
 MEASURED_TRAFFIC = {   # workload[@ranges] -> {"bytes": int, "sha256": str, "profile": str}
     "b128_u1024_8192_paged": {
-        "bytes": 692623104 + 26407936 + 36341760,
-        "sha256": "f0be339353ea62562caede51eaad06f770b741a5f5abb3a6c390f7a56b4faf70",
+        "bytes": 692737536 + 26730752 + 36341760,
+        "sha256": "718942ef98c3b9e43adddeb17c4c750231abb198ff23025d2da1dbaf94bc3095",
         "profile": "profiles/decode_tc_b128_u1024_8192_paged.md (decode + combine, ncu cache flush per kernel)"},
     "b32_l4096": {
-        "bytes": 155803648 + 3008256 + 16865280,
-        "sha256": "f0be339353ea62562caede51eaad06f770b741a5f5abb3a6c390f7a56b4faf70",
+        "bytes": 155795968 + 3335424 + 16865024,
+        "sha256": "718942ef98c3b9e43adddeb17c4c750231abb198ff23025d2da1dbaf94bc3095",
         "profile": "profiles/decode_tc_b32_l4096.md (decode + combine, ncu cache flush per kernel)"},
 }
 
