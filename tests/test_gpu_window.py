@@ -246,3 +246,12 @@ def test_fp8_rows_of_any_scale_have_the_bits_of_their_bf16_values(m, window):
     a, b = call(m, coded, q, window, 4), call(m, plain, q, window, 4)
     assert torch.isfinite(a[1]).all() and (a[0] != 0).any(dim=2).all()
     assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+def test_the_default_stream_argument_is_the_current_stream(m):
+    torch.zeros(1, device="cuda")
+    side = torch.cuda.Stream()
+    assert m._stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert m._stream(None) == side.cuda_stream
+    assert m._stream(None) == torch.cuda.current_stream().cuda_stream
