@@ -826,14 +826,23 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     bool direct;
     float m, l;
   } done = {};
-  // Every warp passes the same barriers.  free_buf: the sums exchange (a maxima buffer not in use).
+  // A wait that runs out (at its own time in every warp, and in some waits of some warps only) ends this
+  // warp's waits, arrivals and output, never its way through the tiles: all eight warps pass the same named
+  // barriers whatever happens, and one that left alone would strand the others there.
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity, site))) {
+      ok = false;
+      *abort_flag = 1;
+    }
+  };
+  // rl: the sums exchange (a maxima buffer not in use).
   auto epilogue = [&](int kd, float* rl) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_final, static_cast<uint32_t>(kd) & 1u, 0x33))) ok = false;
+    wait(&bars->o_final, static_cast<uint32_t>(kd) & 1u, 0x33);
     tc_fence_after();
     rl[me] = done.l;
     named_bar_sync(1, 256);
     const float l_tot = (done.l + rl[me ^ 64]) + (rl[me ^ 128] + rl[me ^ 192]);
-    if (ok && !*abort_flag) {
+    if (__all_sync(0xffffffffu, ok && !*abort_flag)) {   // (the same for the whole warp)
       const int64_t h = 64 * static_cast<int>(rank) + hl;
       if (done.direct) {
         const int64_t bh = static_cast<int64_t>(done.b) * kHeads + h;
@@ -853,12 +862,9 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   float l_run = 0.f;
   for (int d = 1; d < kTcPfDist && d < n_tiles; ++d)
     tc_prefetch_tile<kMapped>(a, map, sg.b, t_begin + d * kTcTile + 64 * static_cast<int>(rank), t_end);
-  for (int i = 0; i < n_tiles && ok; ++i, ++g) {
+  for (int i = 0; i < n_tiles; ++i, ++g) {
     const int j = g & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[j], static_cast<uint32_t>(g >> 1) & 1u, 0x30))) {
-      ok = false;
-      break;
-    }
+    wait(&bars->s_full[j], static_cast<uint32_t>(g >> 1) & 1u, 0x30);
     tc_fence_after();
     float sc[32];
     {
@@ -873,7 +879,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     // arrival orders nothing else, so it is relaxed.
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_relaxed(lbar(&bars->s_empty[j]));
+    if (ok && lane == 0) mbar_arrive_relaxed(lbar(&bars->s_empty[j]));
     // Tokens at or past the split end (only in a ragged last tile) get a score of -inf.
     const int tok0 = t_begin + i * kTcTile + 64 * half + 32 * ch;
     const int nvalid = t_end - tok0;
@@ -914,10 +920,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       // segment never rescales).  Waiting on phase g-1 by parity is unambiguous: PV(g-2) is done
       // (tile g-1 waited for it before writing P) and PV(g) needs this tile's P, so o_ready has
       // completed g-1 or g phases.
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_ready, static_cast<uint32_t>(g - 1) & 1u, 0x31))) {
-        ok = false;
-        break;
-      }
+      wait(&bars->o_ready, static_cast<uint32_t>(g - 1) & 1u, 0x31);
       tc_fence_after();
       tc_rescale_o(tmem + lane_base + kTcColO + 128 * ch, alpha);
     }
@@ -943,24 +946,19 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       epilogue(k - 1, red + (j ^ 1) * 256);
       tc_fence_before();
       named_bar_sync(1, 256);
-      if (!ok) break;
-      if (lane == 0) {
+      if (ok && lane == 0) {
         fence_release_smem_to_cluster();
         mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 0));
         mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 1));
       }
-    } else if (g >= 1 &&
-               !__all_sync(0xffffffffu, mbar_wait(&bars->p_empty[0], static_cast<uint32_t>(g - 1) & 1u, 0x32))) {
-      ok = false;
-      break;
+    } else if (g >= 1) {
+      wait(&bars->p_empty[0], static_cast<uint32_t>(g - 1) & 1u, 0x32);
     }
     if (half == 1) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(lbar(&bars->p_full[0]));
-      // (only these warps wait here: a failure is left to the waits that all of them share)
-      if (g >= 1 && !mbar_wait(&bars->p_empty[1], static_cast<uint32_t>(g - 1) & 1u, 0x34)) *abort_flag = 1;
-      __syncwarp();
+      if (ok && lane == 0) mbar_arrive_relaxed(lbar(&bars->p_full[0]));
+      if (g >= 1) wait(&bars->p_empty[1], static_cast<uint32_t>(g - 1) & 1u, 0x34);
     }
     uint8_t* prow = smem + kTcOffP + half * kTcSlab + hl * 128;
 #pragma unroll
@@ -977,17 +975,13 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
+    if (ok && lane == 0) {
       fence_release_smem_to_cluster();
       mbar_arrive_relaxed(lbar(&bars->p_full[half]));
     }
     if (i + kTcPfDist < n_tiles)
       tc_prefetch_tile<kMapped>(a, map, sg.b, t_begin + (i + kTcPfDist) * kTcTile + 64 * static_cast<int>(rank), t_end);
   }
-  // Leave only on `ok`, which every softmax warp reaches at the same wait (they all wait on the
-  // same barriers), never on the abort flag, which warps may read at different moments: a warp
-  // leaving alone would strand the others at the next named barrier.
-  if (!ok) break;
   done.b = sg.b;
   done.slot = sg.slot;
   done.direct = sg.direct;
@@ -996,7 +990,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   ++k;
   more = cur.next(a.seq_lens, a.capacity, rows, sg);
   }
-  if (ok && k > 0) epilogue(k - 1, red + (g & 1) * 256);   // the buffer the last tile did not use
+  if (k > 0) epilogue(k - 1, red + (g & 1) * 256);   // the buffer the last tile did not use
 }
 
 // A call of one range has no split rows and is not followed by a combine: its empty rows are written here.
