@@ -802,6 +802,21 @@ __device__ __noinline__ void tc_rescale_o(uint32_t addr, float alpha) {
   tmem_st_wait();
 }
 
+// How a softmax warp leaves whose bounded wait ran out.  The eight warps do not give up together (some waits
+// are those of some warps only, and the limit runs out at its own time in each), and the others still meet
+// at named barriers: it passes all of these, without further waits, arrivals or output.  They are
+// `pending` in the current tile, one in each later tile of the segment (`tiles`), two more where a segment
+// follows another, and the last epilogue's.
+template <class Rows>
+__device__ __noinline__ void tc_softmax_leave(SegmentCursor cur, const int32_t* seq_lens, int capacity, const Rows rows,
+                                              int pending, int tiles, volatile int* abort_flag) {
+  *abort_flag = 1;
+  Segment sg;
+  int left = pending + tiles + 1;
+  while (cur.next(seq_lens, capacity, rows, sg)) left += 2 + sg.n_tiles;
+  for (; left > 0; --left) named_bar_sync(1, 256);
+}
+
 template <bool kMapped, class Rows>
 __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, uint8_t* smem, TcBars* bars,
                            float* red, uint32_t tmem, uint32_t rank, volatile int* abort_flag) {
@@ -817,8 +832,13 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   Segment sg;
   int g = 0;   // global tile index of the range
   int k = 0;   // segment index
-  bool ok = true;
   const Rows rows = tc_rows<Rows>(a);
+  auto wait = [&](uint64_t* bar, int n, uint32_t site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(n) & 1u, site));
+  };
+  auto leave = [&](int pending, int tiles) {
+    tc_softmax_leave(cur, a.seq_lens, a.capacity, rows, pending, tiles, abort_flag);
+  };
   // The segment whose tiles are done but whose O has not been read.  Its epilogue runs once the next
   // segment's first P is in registers, so that the wait for the last PV overlaps that softmax.
   struct {
@@ -826,23 +846,14 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     bool direct;
     float m, l;
   } done = {};
-  // A wait that runs out (at its own time in every warp, and in some waits of some warps only) ends this
-  // warp's waits, arrivals and output, never its way through the tiles: all eight warps pass the same named
-  // barriers whatever happens, and one that left alone would strand the others there.
-  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-    if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity, site))) {
-      ok = false;
-      *abort_flag = 1;
-    }
-  };
-  // rl: the sums exchange (a maxima buffer not in use).
-  auto epilogue = [&](int kd, float* rl) {
-    wait(&bars->o_final, static_cast<uint32_t>(kd) & 1u, 0x33);
+  // rl: the sums exchange (a maxima buffer not in use).  False, before its barrier, if the wait ran out.
+  auto epilogue = [&](int kd, float* rl) -> bool {
+    if (!wait(&bars->o_final, kd, 0x33)) return false;
     tc_fence_after();
     rl[me] = done.l;
     named_bar_sync(1, 256);
     const float l_tot = (done.l + rl[me ^ 64]) + (rl[me ^ 128] + rl[me ^ 192]);
-    if (__all_sync(0xffffffffu, ok && !*abort_flag)) {   // (the same for the whole warp)
+    if (__all_sync(0xffffffffu, !*abort_flag)) {   // (the same for the whole warp)
       const int64_t h = 64 * static_cast<int>(rank) + hl;
       if (done.direct) {
         const int64_t bh = static_cast<int64_t>(done.b) * kHeads + h;
@@ -853,6 +864,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
         tc_write_segment(false, a.ws.o + ml * kDLat, a.ws.m + ml, a.ws.l + ml, smem, tmem, done.m, l_tot);
       }
     }
+    return true;
   };
   bool more = cur.next(a.seq_lens, a.capacity, rows, sg);
   while (more) {
@@ -864,7 +876,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     tc_prefetch_tile<kMapped>(a, map, sg.b, t_begin + d * kTcTile + 64 * static_cast<int>(rank), t_end);
   for (int i = 0; i < n_tiles; ++i, ++g) {
     const int j = g & 1;
-    wait(&bars->s_full[j], static_cast<uint32_t>(g >> 1) & 1u, 0x30);
+    if (!wait(&bars->s_full[j], g >> 1, 0x30)) return leave(i == 0 && k > 0 ? 3 : 1, n_tiles - i - 1);
     tc_fence_after();
     float sc[32];
     {
@@ -879,7 +891,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     // arrival orders nothing else, so it is relaxed.
     tc_fence_before();
     __syncwarp();
-    if (ok && lane == 0) mbar_arrive_relaxed(lbar(&bars->s_empty[j]));
+    if (lane == 0) mbar_arrive_relaxed(lbar(&bars->s_empty[j]));
     // Tokens at or past the split end (only in a ragged last tile) get a score of -inf.
     const int tok0 = t_begin + i * kTcTile + 64 * half + 32 * ch;
     const int nvalid = t_end - tok0;
@@ -920,7 +932,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       // segment never rescales).  Waiting on phase g-1 by parity is unambiguous: PV(g-2) is done
       // (tile g-1 waited for it before writing P) and PV(g) needs this tile's P, so o_ready has
       // completed g-1 or g phases.
-      wait(&bars->o_ready, static_cast<uint32_t>(g - 1) & 1u, 0x31);
+      if (!wait(&bars->o_ready, g - 1, 0x31)) return leave(0, n_tiles - i - 1);
       tc_fence_after();
       tc_rescale_o(tmem + lane_base + kTcColO + 128 * ch, alpha);
     }
@@ -943,22 +955,22 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     // Between segments the epilogue waits for more (all of PV), reads O and stages it through the
     // P buffer; the barrier then lets every warp write P, and both CTAs learn that O may be overwritten.
     if (i == 0 && k > 0) {
-      epilogue(k - 1, red + (j ^ 1) * 256);
+      if (!epilogue(k - 1, red + (j ^ 1) * 256)) return leave(2, n_tiles - i - 1);
       tc_fence_before();
       named_bar_sync(1, 256);
-      if (ok && lane == 0) {
+      if (lane == 0) {
         fence_release_smem_to_cluster();
         mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 0));
         mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 1));
       }
-    } else if (g >= 1) {
-      wait(&bars->p_empty[0], static_cast<uint32_t>(g - 1) & 1u, 0x32);
+    } else if (g >= 1 && !wait(&bars->p_empty[0], g - 1, 0x32)) {
+      return leave(0, n_tiles - i - 1);
     }
     if (half == 1) {
       tc_fence_before();
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive_relaxed(lbar(&bars->p_full[0]));
-      if (g >= 1) wait(&bars->p_empty[1], static_cast<uint32_t>(g - 1) & 1u, 0x34);
+      if (lane == 0) mbar_arrive_relaxed(lbar(&bars->p_full[0]));
+      if (g >= 1 && !wait(&bars->p_empty[1], g - 1, 0x34)) return leave(0, n_tiles - i - 1);
     }
     uint8_t* prow = smem + kTcOffP + half * kTcSlab + hl * 128;
 #pragma unroll
@@ -975,7 +987,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
-    if (ok && lane == 0) {
+    if (lane == 0) {
       fence_release_smem_to_cluster();
       mbar_arrive_relaxed(lbar(&bars->p_full[half]));
     }
@@ -990,7 +1002,7 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   ++k;
   more = cur.next(a.seq_lens, a.capacity, rows, sg);
   }
-  if (k > 0) epilogue(k - 1, red + (g & 1) * 256);   // the buffer the last tile did not use
+  if (k > 0 && !epilogue(k - 1, red + (g & 1) * 256)) leave(0, 0);   // (the buffer the last tile did not use)
 }
 
 // A call of one range has no split rows and is not followed by a combine: its empty rows are written here.

@@ -2,7 +2,7 @@
 meet at a named barrier in every tile, so a warp whose wait ran out must keep passing the barriers of the
 others: a warp that left alone would strand them there for good.
 
-`tc_softmax` is taken from the kernel's source as it stands and compiled for the host, a thread per warp
+`tc_softmax` and `tc_softmax_leave` are taken from the kernel's source as they stand and compiled for the host, a thread per warp
 (its lane 0), with the PTX wrappers replaced by stand-ins: a wait gives up where the scenario says so (on
 all warps, or on one, whose clock ran out first), and the named barrier reports a warp that is never joined.
 """
@@ -204,7 +204,8 @@ def softmax(tmp_path_factory):
     with open(os.path.join(CSRC, "decode_tc.cuh")) as f:
         src = f.read()
     constants = "\n".join(re.findall(r"^constexpr (?:int|uint32_t|float) kTc\w+ = [^;]*;", src, re.M))
-    code = block(src, "template <bool kMapped, class Rows>\n__device__ void tc_softmax")
+    code = block(src, "template <class Rows>\n__device__ __noinline__ void tc_softmax_leave") + "\n" + block(
+        src, "template <bool kMapped, class Rows>\n__device__ void tc_softmax(")
     where = tmp_path_factory.mktemp("softmax")
     cpp, exe = str(where / "softmax.cpp"), str(where / "softmax")
     with open(cpp, "w") as f:
