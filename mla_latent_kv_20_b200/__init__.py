@@ -314,15 +314,26 @@ def evict_workspace_size(batch: int, keep: int) -> int:
     return lib.mla_evict_workspace_size(batch, keep)
 
 
+def _in_place(desc, block_table, desc_out, block_table_out):
+    """The output's descriptor and block table of an eviction within one buffer: the source's where none is
+    given (its table only where the output's descriptor has rows of that width)."""
+    if desc_out is None:
+        desc_out = desc
+    if block_table_out is None and desc_out.max_blocks_per_seq == desc.max_blocks_per_seq:
+        block_table_out = block_table
+    return desc_out, block_table_out
+
+
 def cache_evict(cache, seq_lens, weights, desc: CacheDesc, kept, lens_out, weights_out, workspace, *, keep: int,
                 sinks: int = 0, recent: int = 0, block_table=None, cache_out=None, desc_out: CacheDesc | None = None,
                 block_table_out=None, stream=None, batch: int | None = None, workspace_bytes: int | None = None):
     """mla_cache_evict: each sequence longer than `keep` keeps its first `sinks`, its last `recent` and the
-    heaviest tokens between, moved in order to the front of cache_out, or (cache_out None) of the same cache."""
+    heaviest tokens between, moved in order to the front of cache_out, or (cache_out None) of the same cache; there
+    block_table_out, with desc_out unless it is as wide as block_table, may name fresh pages of the same pool."""
     b = seq_lens.shape[0] if batch is None else batch
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
     if cache_out is None:
-        cache_out, desc_out, block_table_out = cache, desc, block_table
+        cache_out, desc_out, block_table_out = cache, *_in_place(desc, block_table, desc_out, block_table_out)
     _check(lib.mla_cache_evict(_ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(weights), desc, b, keep, sinks,
                                recent, _ptr(cache_out), _ptr(block_table_out), desc_out, _ptr(kept), _ptr(lens_out),
                                _ptr(weights_out), _ptr(workspace), wb, _stream(stream)), "mla_cache_evict")
@@ -336,7 +347,8 @@ def cache_evict_fp8(cache, scales, seq_lens, weights, desc: CacheDesc, kept, len
     b = seq_lens.shape[0] if batch is None else batch
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
     if cache_out is None:
-        cache_out, scales_out, desc_out, block_table_out = cache, scales, desc, block_table
+        cache_out, scales_out = cache, scales if scales_out is None else scales_out
+        desc_out, block_table_out = _in_place(desc, block_table, desc_out, block_table_out)
     _check(lib.mla_cache_evict_fp8(_ptr(cache), _ptr(scales), _ptr(block_table), _ptr(seq_lens), _ptr(weights), desc, b,
                                    keep, sinks, recent, _ptr(cache_out), _ptr(scales_out), _ptr(block_table_out),
                                    desc_out, _ptr(kept), _ptr(lens_out), _ptr(weights_out), _ptr(workspace), wb,

@@ -1,4 +1,9 @@
 """Host side of the eviction and of the append at a slot: their refusals and the workspace's size."""
+import types
+
+import pytest
+import torch
+
 from test_abi_cpu import FAKE, host_only, mla  # noqa: F401  (fixtures)
 
 FAR = 1 << 40
@@ -62,3 +67,53 @@ def test_append_at_refusals(host_only):  # noqa: F811
     assert lib.mla_cache_append_at(FAKE, FAKE, None, FAKE, FAKE, FAKE, None, d, 5, 10000.0, None) == 1
     assert lib.mla_cache_append_at_fp8(FAKE, FAKE, None, FAKE, None, FAKE, FAKE, None, d, 4, 10000.0, None) == 1
     assert lib.mla_cache_append_at_fp8(FAKE, FAKE, None, FAKE, FAKE, FAKE, None, None, d, 4, 10000.0, None) == 1
+
+
+@pytest.fixture
+def passed(mla, monkeypatch):  # noqa: F811
+    """Calls the binding with a library that only notes what it is given."""
+    def call(fp8, **kw):
+        got = {}
+
+        def note(*args):
+            names = ["cache", *(["scales"] if fp8 else []), "table", "lens", "weights", "desc", "batch", "keep", "sinks",
+                     "recent", "out", *(["scales_out"] if fp8 else []), "table_out", "desc_out"]
+            got.update(zip(names, args))
+            return 0
+
+        monkeypatch.setattr(mla, "lib", types.SimpleNamespace(mla_cache_evict=note, mla_cache_evict_fp8=note))
+        lens, ws = torch.zeros(3, dtype=torch.int32), torch.zeros(64, dtype=torch.uint8)
+        args = (lens, FAKE, mla.paged_desc(3, 8, 24), FAKE, FAKE, FAKE, ws)
+        kw = dict(keep=64, block_table=0x200, stream=0, **kw)
+        if fp8:
+            mla.cache_evict_fp8(0x100, 0x110, *args, **kw)
+        else:
+            mla.cache_evict(0x100, *args, **kw)
+        return got
+
+    return call
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_binding_in_place_takes_what_is_given(mla, passed, fp8):  # noqa: F811
+    got = passed(fp8)
+    assert got["out"] == 0x100 and got["table_out"] == 0x200 and got["desc_out"].max_blocks_per_seq == 8
+    assert not fp8 or got["scales_out"] == 0x110
+    # the same pool, other pages
+    got = passed(fp8, desc_out=mla.paged_desc(3, 2, 24), block_table_out=0x300)
+    assert got["out"] == 0x100 and got["table_out"] == 0x300 and got["desc_out"].max_blocks_per_seq == 2
+    got = passed(fp8, block_table_out=0x300)   # as wide as the old table
+    assert got["table_out"] == 0x300 and got["desc_out"].max_blocks_per_seq == 8
+    # a narrower descriptor does not fit the source's table: no table, which the library refuses
+    assert passed(fp8, desc_out=mla.paged_desc(3, 2, 24))["table_out"] is None
+    assert passed(fp8, desc_out=mla.paged_desc(3, 8, 24))["table_out"] == 0x200
+    if fp8:   # (and the library refuses one buffer of codes with two of scales)
+        assert passed(fp8, scales_out=0x120)["scales_out"] == 0x120
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_binding_into_another_cache(mla, passed, fp8):  # noqa: F811
+    kw = dict(scales_out=0x410) if fp8 else {}
+    got = passed(fp8, cache_out=0x400, desc_out=mla.paged_desc(3, 2, 6), block_table_out=0x300, **kw)
+    assert got["out"] == 0x400 and got["table_out"] == 0x300 and got["desc_out"].num_rows == 6 * 64
+    assert passed(fp8, cache_out=0x400, desc_out=mla.contiguous_desc(3, 128), **kw)["table_out"] is None

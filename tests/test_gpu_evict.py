@@ -314,3 +314,36 @@ def test_append_at_refuses_slots_outside(m):
                           block_table=cache.table)
         assert m.get_device_error() & m.DEVERR_POS_RANGE
         assert np.array_equal(bits(cache.data), before)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_fresh_pages_named_without_the_cache(m, fp8):
+    """block_table_out and desc_out alone: the rows land in those pages, the old ones keep theirs."""
+    rng = np.random.default_rng(23)
+    lens, keep = [500, 130, 64], 100
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 24, fp8=fp8)
+    used = set(cache.table[cache.table >= 0].cpu().tolist())
+    free = [p for p in range(cache.data.shape[0] // 64) if p not in used][:6]
+    assert len(free) == 6
+    tab = np.array(free, np.int32).reshape(3, 2)
+    w = weights_like(rng, 3, cache.capacity, "heavy").cuda()
+    rows, scales = bits(cache.data), None if not fp8 else bits(cache.scales)
+    kept = torch.zeros((3, keep), dtype=torch.int32, device="cuda")
+    lens_out = torch.zeros((3,), dtype=torch.int32, device="cuda")
+    wo = torch.zeros((3, 128), device="cuda")
+    ws = torch.empty((m.evict_workspace_size(3, keep),), dtype=torch.uint8, device="cuda")
+    call = m.cache_evict_fp8 if fp8 else m.cache_evict
+    call(cache.data, *([cache.scales] if fp8 else []), cache.seq_lens, w, cache.desc, kept, lens_out, wo, ws, keep=keep,
+         sinks=2, recent=20, block_table=cache.table, block_table_out=torch.from_numpy(tab).cuda(),
+         desc_out=m.paged_desc(3, 2, cache.data.shape[0] // 64))
+    assert m.get_device_error() == 0
+    for b, L in enumerate(lens):
+        t = oracle.evict_keep(w[b].cpu().numpy(), L, keep, 2, 20)
+        j = np.arange(len(t))
+        to, frm = tab[b][j // 64].astype(np.int64) * 64 + j % 64, cache.rows_of(b, t).numpy()
+        rows[to] = rows[frm]
+        if fp8:
+            scales[to] = scales[frm]
+    assert np.array_equal(bits(cache.data), rows)
+    if fp8:
+        assert np.array_equal(bits(cache.scales), scales)
