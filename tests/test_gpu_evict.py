@@ -347,3 +347,43 @@ def test_fresh_pages_named_without_the_cache(m, fp8):
     assert np.array_equal(bits(cache.data), rows)
     if fp8:
         assert np.array_equal(bits(cache.scales), scales)
+
+
+# Sequences whose selection a cluster of CTAs shares (more than 4096 tokens of capacity each): rows, scales and
+# weights as they are after it, moved by the selection itself (up to 128 kept tokens) or by a second launch.
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,keep,sinks,recent", [([9000, 60, 0], 64, 4, 16), ([40000], 128, 0, 33),
+                                                    ([9000, 129, 5000], 128, 60, 68), ([4100, 9000], 1, 0, 0),
+                                                    ([9000, 300], 129, 3, 40), ([20000, 1500], 1000, 5, 100)])
+def test_rows_of_sequences_shared_by_a_cluster(m, lens, keep, sinks, recent, in_place, fp8):
+    check(m, lens, True, fp8, in_place, "heavy", keep, sinks, recent, keep + len(lens))
+
+
+@pytest.mark.parametrize("kind", ["few", "special"])
+def test_ties_of_sequences_shared_by_a_cluster(m, kind):
+    check(m, [9000, 4500], False, False, True, kind, 100, 2, 10, 31)
+    check(m, [9000, 4500], True, False, False, kind, 100, 0, 0, 32)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("keep", [96, 200])
+def test_weights_and_lengths_in_place_of_a_sequence_shared_by_a_cluster(m, keep, fp8):
+    """weights_out = weights and lens_out = seq_lens."""
+    rng = np.random.default_rng(41)
+    lens = [9000, 150, 5000]
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 42, fp8=fp8)
+    first = bits(cache.data)
+    w = weights_like(rng, 3, cache.capacity, "heavy").cuda()
+    w0 = w.cpu().numpy()
+    kept, _, _ = evict(m, cache, w, keep, 4, 30, None, w, cache.seq_lens)
+    assert m.get_device_error() == 0
+    assert cache.seq_lens.tolist() == [min(L, keep) for L in lens]
+    got, rows = bits(w), bits(cache.data)
+    for b, L in enumerate(lens):
+        t = oracle.evict_keep(w0[b], L, keep, 4, 30)
+        n = len(t)
+        assert kept[b].tolist() == list(t) + [-1] * (keep - n)
+        assert np.array_equal(got[b, :n], w0[b][t].view(np.int32)) and np.all(got[b, n:L] == 0)
+        assert np.array_equal(got[b, L:], w0[b][L:].view(np.int32))
+        assert np.array_equal(rows[cache.rows_of(b, np.arange(n)).numpy()], first[cache.rows_of(b, t).numpy()])
