@@ -753,7 +753,8 @@ mla_status launch_evict(const void* cache, const uint8_t* scales, const int32_t*
   const mla::EvictWorkspace ws = mla::ev_carve(workspace, batch, keep);
   const mla::EvictCache src{v, static_cast<uint8_t*>(const_cast<void*>(cache)), const_cast<uint8_t*>(scales)};
   const mla::EvictCache dst{vo, static_cast<uint8_t*>(cache_out), scales_out};
-  const bool moved = keep <= mla::kEvMoveRows;   // by the selection itself
+  const int slots = std::min(keep, capacity);      // that may hold a row: what the launches follow
+  const bool moved = slots <= mla::kEvMoveRows;    // by the selection itself
   auto select = !moved ? mla::evict_select_kernel<0>
                        : (fp8 ? mla::evict_select_kernel<mla::kDRow> : mla::evict_select_kernel<2 * mla::kDRow>);
   if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -769,7 +770,7 @@ mla_status launch_evict(const void* cache, const uint8_t* scales, const int32_t*
                           dim3(9, batch), dim3(256), 0, s, src, dst, static_cast<const int32_t*>(kept), ws, keep,
                           capacity_out, weights_out, lens_out);
   return launch_chained(fp8 ? mla::evict_copy_kernel<mla::kDRow> : mla::evict_copy_kernel<2 * mla::kDRow>,
-                        dim3((keep + mla::kEvRows - 1) / mla::kEvRows, batch), dim3(256), 0, s, src, dst,
+                        dim3((slots + mla::kEvRows - 1) / mla::kEvRows, batch), dim3(256), 0, s, src, dst,
                         static_cast<const int32_t*>(kept), ws, keep, capacity_out, weights_out, lens_out);
 }
 

@@ -1,5 +1,7 @@
 """Eviction by accumulated attention weight (mla_cache_evict, _fp8) and the append at a slot of its own
 (mla_cache_append_at, _fp8): every output is a copy or a whole number, so all comparisons are of bits."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -387,3 +389,54 @@ def test_weights_and_lengths_in_place_of_a_sequence_shared_by_a_cluster(m, keep,
         assert np.array_equal(got[b, :n], w0[b][t].view(np.int32)) and np.all(got[b, n:L] == 0)
         assert np.array_equal(got[b, L:], w0[b][L:].view(np.int32))
         assert np.array_equal(rows[cache.rows_of(b, np.arange(n)).numpy()], first[cache.rows_of(b, t).numpy()])
+
+
+class KernelNodeParams(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                ("shared", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
+                ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+def launches(graph):
+    """The grids of the kernels of a captured graph."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    raw = ctypes.c_void_p(graph.raw_cuda_graph())
+    n = ctypes.c_size_t(0)
+    assert cu.cuGraphGetNodes(raw, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
+    grids = []
+    for node in nodes:
+        kind, p = ctypes.c_int(-1), KernelNodeParams()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value == 0:   # a kernel
+            assert cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+            grids.append(tuple(p.grid))
+    return grids
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,blocks", [([100, 128], None), ([300, 1000], 32)])   # blocks of 32 of 1024 slots
+def test_keep_beyond_the_capacity_costs_no_launches(m, lens, blocks, fp8):
+    """What is launched follows min(keep, capacity): the slots that can hold a row."""
+    rng = np.random.default_rng(51)
+    keep = 1 << 18
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 52, fp8=fp8)
+    out = RowCache(m, [random_rows(rng, cache.capacity) for _ in lens], True, 53, fp8=fp8)
+    w = weights_like(rng, 2, cache.capacity, "heavy").cuda()
+    evict(m, cache, w, keep, 4, 8, out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g, stream=side):
+        kept, lens_out, wo = evict(m, cache, w, keep, 4, 8, out)
+    moves = [x for x in launches(g) if x[1] == len(lens)]   # (blocks of slots, sequences)
+    g.replay()
+    torch.cuda.synchronize()
+    assert m.get_device_error() == 0 and lens_out.tolist() == lens
+    for b, L in enumerate(lens):
+        assert kept[b, :L].tolist() == list(range(L)) and torch.all(kept[b, L:] == -1)
+        assert np.array_equal(bits(out.data)[out.rows_of(b, np.arange(L)).numpy()],
+                              bits(cache.data)[cache.rows_of(b, np.arange(L)).numpy()])
+    # (the selection itself moves the rows of a cache of at most 128 slots)
+    assert moves == ([] if blocks is None else [(blocks, len(lens), 1)])
