@@ -205,7 +205,8 @@ struct SegmentCursor {
 //   out = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p,   M = max_p m_p,   in ascending range order.
 // kByRange: block x < P takes the row whose first piece range x holds, if it is split (fewer rows are split
 // than there are ranges), looked up in the plan table, and the blocks from P on look over 32 rows each
-// for empty ones; otherwise block x takes row x.  A warp covers 128 kCols latent columns of a head (a lane kCols pieces of four), a block
+// for empty ones; otherwise block x takes row x.  An empty row is written by the blocks y of its x, kCols
+// heads each (one block a row: 4000 rows of nothing 286 us, 127 now).  A warp covers 128 kCols latent columns of a head (a lane kCols pieces of four), a block
 // of four warps kCols heads: kCols = 4 where there are rows enough to fill the device, 1 where few rows
 // may have many partials each.  8 / kCols partials are in flight at a time; their m and l are read by
 // lane i for the row's i-th range, 32 ranges at once.
@@ -218,17 +219,16 @@ __global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int P, int B
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   auto write_empty = [&](int b) {
-    const int64_t row = static_cast<int64_t>(b) * kHeads;
-    for (int i = threadIdx.x; i < kHeads * kDLat / 8; i += 128)
+    const int64_t row = static_cast<int64_t>(b) * kHeads + blockIdx.y * kCols;
+    for (int i = threadIdx.x; i < kCols * kDLat / 8; i += 128)
       reinterpret_cast<uint4*>(out_lat + row * kDLat)[i] = make_uint4(0, 0, 0, 0);
-    if (lse != nullptr) lse[row + threadIdx.x] = -INFINITY;
+    if (lse != nullptr && threadIdx.x < kCols) lse[row + threadIdx.x] = -INFINITY;
   };
   const bool per_seq = ws.off[B + 1] == kPlanPerSequence;
   const int C = ws.off[B];
   int b = blockIdx.x, p0;
   if (kByRange) {
     if (blockIdx.x >= P) {
-      if (blockIdx.y != 0) return;
       const int b0 = 32 * (static_cast<int>(blockIdx.x) - P);
       uint32_t empty = __ballot_sync(0xffffffffu, b0 + lane < B && ws.off[b0 + lane + 1] == ws.off[b0 + lane]);
       for (; empty != 0; empty &= empty - 1) write_empty(b0 + __ffs(empty) - 1);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int P, int B
   // and a range with x_p = x_{p+1} is empty.
   const int off = ws.off[b], span = ws.off[b + 1] - off;
   if (span == 0) {
-    if (!kByRange && blockIdx.y == 0) write_empty(b);
+    if (!kByRange) write_empty(b);
     return;
   }
   p0 = per_seq ? off : range_of_cost(off + kSegCost, P, C);

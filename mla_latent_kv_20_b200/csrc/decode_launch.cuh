@@ -201,7 +201,7 @@ mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t*
   mla_status ls = launch_chained(kernel, dim3(2 * P), dim3(mla::tc_threads(fp8)),
                                  static_cast<size_t>(mla::kTcSmemBytes), s, tka, tkb, tv, tq, tsc, a);
   if (ls != MLA_OK) return ls;
-  if (P == 1) return MLA_OK;   // one range covers every row
+  if (P == 1 && rows <= mla::kTcOwnEmptyRows) return MLA_OK;   // one range covers every row
   auto* out = reinterpret_cast<__nv_bfloat16*>(out_lat);
   if (rows <= 8)   // few rows, perhaps of many partials
     return launch_chained(mla::combine_kernel<1, false>, dim3(rows, mla::kHeads), dim3(128), 0, s, a.ws, P, rows, out,

@@ -1005,7 +1005,9 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
   if (k > 0 && !epilogue(k - 1, red + (g & 1) * 256)) leave(0, 0);   // (the buffer the last tile did not use)
 }
 
-// A call of one range has no split rows and is not followed by a combine: its empty rows are written here.
+// A call of one range has no split rows.  One of a few rows is not followed by a combine, and its empty
+// rows are written here (each takes the pair about 1 us; a launch takes two).
+constexpr int kTcOwnEmptyRows = 2;
 template <class Rows>
 __device__ void tc_empty_rows(const DecodeTcArgs& a, uint32_t rank) {
   const Rows rows = tc_rows<Rows>(a);
@@ -1293,7 +1295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads(kFp8), 1)
   const bool busy = pl.start < pl.end;   // the same in both CTAs of the pair
   const uint32_t tmem = *tmem_slot;
 
-  if (warp < kTcSoftmaxWarps && a.P == 1) tc_empty_rows<Rows>(a, rank);
+  if (warp < kTcSoftmaxWarps && a.P == 1 && a.batch <= kTcOwnEmptyRows) tc_empty_rows<Rows>(a, rank);
   if (!busy) {
     // an idle range: only the teardown below
   } else if (warp < kTcSoftmaxWarps) {

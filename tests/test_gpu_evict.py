@@ -1,13 +1,11 @@
 """Eviction by accumulated attention weight (mla_cache_evict, _fp8) and the append at a slot of its own
 (mla_cache_append_at, _fp8): every output is a copy or a whole number, so all comparisons are of bits."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
 
 import oracle
-from bounded_common import RowCache, random_rows
+from bounded_common import RowCache, launches, random_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -389,30 +387,6 @@ def test_weights_and_lengths_in_place_of_a_sequence_shared_by_a_cluster(m, keep,
         assert np.array_equal(got[b, :n], w0[b][t].view(np.int32)) and np.all(got[b, n:L] == 0)
         assert np.array_equal(got[b, L:], w0[b][L:].view(np.int32))
         assert np.array_equal(rows[cache.rows_of(b, np.arange(n)).numpy()], first[cache.rows_of(b, t).numpy()])
-
-
-class KernelNodeParams(ctypes.Structure):
-    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
-                ("shared", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
-                ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
-
-
-def launches(graph):
-    """The grids of the kernels of a captured graph."""
-    cu = ctypes.CDLL("libcuda.so.1")
-    raw = ctypes.c_void_p(graph.raw_cuda_graph())
-    n = ctypes.c_size_t(0)
-    assert cu.cuGraphGetNodes(raw, None, ctypes.byref(n)) == 0
-    nodes = (ctypes.c_void_p * n.value)()
-    assert cu.cuGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
-    grids = []
-    for node in nodes:
-        kind, p = ctypes.c_int(-1), KernelNodeParams()
-        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
-        if kind.value == 0:   # a kernel
-            assert cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
-            grids.append(tuple(p.grid))
-    return grids
 
 
 @pytest.mark.parametrize("fp8", [False, True])

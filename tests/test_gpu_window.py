@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from bounded_common import SCALE, RowCache, assert_window_row, f64, random_q, random_rows
+from bounded_common import SCALE, RowCache, assert_window_row, f64, launches, random_q, random_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -255,3 +255,52 @@ def test_the_default_stream_argument_is_the_current_stream(m):
     with torch.cuda.stream(side):
         assert m._stream(None) == side.cuda_stream
     assert m._stream(None) == torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("form", ["one range", "nothing visible", "many rows", "fewer rows than ranges"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_empty_rows_are_written_by_the_whole_device(m, form, fp8):
+    """Zeros and -inf for every empty row, from blocks enough to write them quickly, and the other rows as ever."""
+    rows = 40 if form == "fewer rows than ranges" else 500
+    lens = [0] * rows
+    if form != "nothing visible":
+        lens[7], lens[rows - 1] = 130, 64
+    rng = np.random.default_rng(71)
+    cache = RowCache(m, [random_rows(rng, L) for L in lens], True, 72, fp8=fp8,
+                     max_len=4096 if form == "fewer rows than ranges" else None)
+    q = random_q(rng, rows).cuda()
+    out = torch.full((rows, 128, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, 128), float("nan"), device="cuda")
+    ws = torch.empty((m.decode_workspace_size(rows, cache.capacity),), dtype=torch.uint8, device="cuda")
+    kw = dict(lse=lse, block_table=cache.table, num_splits=1 if form == "one range" else 0)
+    if form == "nothing visible":
+        cache.seq_lens.fill_(64)
+        kw.update(window=0, sinks=0)
+
+    def call():
+        args = (cache.seq_lens, cache.desc, ws, out)
+        if fp8:
+            f = m.decode_attn_window_fp8 if "window" in kw else m.decode_attn_fp8
+            f(q, cache.data, cache.scales, *args, **kw)
+        else:
+            (m.decode_attn_window if "window" in kw else m.decode_attn)(q, cache.data, *args, **kw)
+
+    call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g, stream=side):
+        call()
+    out.fill_(float("nan"))
+    lse.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    assert m.get_device_error() == 0
+    full = [b for b, L in enumerate(lens) if L]
+    empty = torch.ones(rows, dtype=torch.bool)
+    empty[full] = False
+    assert torch.all(out[empty.cuda()] == 0) and torch.all(torch.isneginf(lse[empty.cuda()]))
+    for b in full:
+        assert_window_row(f64(out[b]), f64(lse[b]),
+                          oracle.window_rows(f64(q[b]), cache.values[b], 10 ** 6, 0, SCALE, 512))
+    assert max(x * y for x, y, _ in launches(g)) >= rows
