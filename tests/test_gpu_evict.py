@@ -414,3 +414,11 @@ def test_keep_beyond_the_capacity_costs_no_launches(m, lens, blocks, fp8):
                               bits(cache.data)[cache.rows_of(b, np.arange(L)).numpy()])
     # (the selection itself moves the rows of a cache of at most 128 slots)
     assert moves == ([] if blocks is None else [(blocks, len(lens), 1)])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[1], [3, 2], [16, 0, 9]])
+def test_caches_of_a_few_slots(m, lens, fp8):
+    for in_place in (False, True):
+        for keep, sinks, recent in ((1, 0, 0), (1, 1, 0), (2, 0, 1)):
+            check(m, lens, False, fp8, in_place, "special", keep, sinks, recent, 61)

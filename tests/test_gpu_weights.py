@@ -384,3 +384,25 @@ def test_a_bounded_conversation(m, fp8, paged):
     for _ in range(3):
         step()
     assert m.get_device_error() == 0
+
+
+@pytest.mark.parametrize("capacity", [1, 3, 8, 9, 16, 60])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_caches_smaller_than_a_copy(m, fp8, capacity):
+    """Buffers of fewer rows than the boxes that are copied from them."""
+    for lens in ([capacity], [capacity, 0, (capacity + 1) // 2]):
+        rng = np.random.default_rng(111)
+        cache = RowCache(m, [random_rows(rng, L) for L in lens], False, 112, fp8=fp8, max_len=capacity, align=1)
+        assert cache.capacity == capacity
+        q = random_q(rng, len(lens))
+        qf = f64(q)
+        lse = np.stack([row_lse(qf[b], cache.values[b]) for b in range(len(lens))])
+        got = call(m, cache, q.cuda(), torch.from_numpy(lse).cuda())
+        assert m.get_device_error() == 0
+        pairs = [weight_sums(qf[b], cache.values[b], lse[b].astype(float)) for b in range(len(lens))]
+        check(f64(got), lens, [x for x, _ in pairs], [x for _, x in pairs], None, 1.0, np.full(got.shape, 7.0))
+        if not fp8:
+            n = len(lens)
+            got = call(m, cache, q.cuda(), torch.from_numpy(lse).cuda(),
+                       q_start=torch.arange(n + 1, dtype=torch.int32, device="cuda"), q_len=cache.seq_lens.clone())
+            check(f64(got), lens, [x for x, _ in pairs], [x for _, x in pairs], None, 1.0, np.full(got.shape, 7.0))
