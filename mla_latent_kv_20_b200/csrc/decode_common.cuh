@@ -101,7 +101,6 @@ struct FullRows {
   static constexpr bool kHoles = false;
   struct Map {
     __device__ __forceinline__ int real(int v) const { return v; }
-    __device__ __forceinline__ bool in_sinks(int) const { return false; }
     __device__ __forceinline__ int hole0() const { return 0; }
     __device__ __forceinline__ int hole1() const { return 0; }
   };
@@ -114,7 +113,6 @@ struct WindowRows {
   struct Map {
     int first, shift, h0, h1;
     __device__ __forceinline__ int real(int v) const { return v < first ? v : v + shift; }
-    __device__ __forceinline__ bool in_sinks(int v) const { return v < first; }
     __device__ __forceinline__ int hole0() const { return h0; }
     __device__ __forceinline__ int hole1() const { return h1; }
   };
@@ -170,9 +168,6 @@ struct SegmentCursor {
   int pair;
   bool first;
   int len0;    // length of the first sequence b (known from the plan: no memory read on the way in)
-
-  // False only if next() will return false (true may still be followed by no segment).
-  __device__ bool may_continue() const { return b < b_end && off < end; }
 
   template <class Rows>
   __device__ bool next(const int32_t* seq_lens, int capacity, const Rows& rows, Segment& s) {

@@ -148,7 +148,7 @@ struct TcBars {
   uint64_t p_empty[2];           // both, per half: PV of a tile done reading P
   uint64_t o_ready;              // both: PV of a tile done writing O (one phase per tile)
   uint64_t o_final;              // both: the last PV of a segment done (one phase per segment)
-  uint64_t o_free;               // both: every softmax warp of both CTAs has read O of a segment
+  uint64_t o_free;               // even CTA only: every softmax warp of both CTAs has read O of a segment
   uint64_t q_full;               // even CTA only: Q of both CTAs landed (one phase per segment)
   uint64_t q_empty;              // both: QK^T of a segment's last tile done
   uint64_t kraw[2];              // FP8, per CTA and part: this CTA's K codes and scales landed (+ tx)
@@ -156,13 +156,6 @@ struct TcBars {
 };
 static_assert(sizeof(TcBars) <= 256, "barrier block");
 static_assert(kTcSmemBytes <= 232448, "shared memory budget");
-
-// Row of (seq b, token t) for a TMA coordinate; -kTcTile (a fully out-of-bounds box, which the
-// TMA unit fills with zeros) when the mapping is invalid.
-__device__ __forceinline__ int tma_row(const CacheView& v, int b, int t) {
-  const int64_t r = cache_row(v, b, t);
-  return r < 0 ? -kTcTile : static_cast<int>(r);
-}
 
 __device__ __forceinline__ uint32_t lbar(const void* p) { return mapa_shared(smem_u32(p), 0); }
 
@@ -317,8 +310,8 @@ __device__ bool tc_producer(const CUtensorMap* tm_ka, const CUtensorMap* tm_kb, 
     }
     // Where the 64-token box at token t (of the frame; boxes never cross a page) lies: its block id, or its
     // row in a contiguous cache.  Fetched a tile ahead, so that neither a copy nor the wait before it
-    // stands behind a dependent load of the block table; turned into the TMA row when it is used (a
-    // fully out-of-bounds box for a bad block id or map entry).
+    // stands behind a dependent load of the block table; turned into the TMA row when it is used (for a bad
+    // block id or map entry that of a fully out-of-bounds box, which the TMA unit fills with zeros).
     const int cb = tc_cache_seq<kMapped>(a, b, !kV);
     const int32_t* table = paged ? a.v.block_table + static_cast<int64_t>(cb < 0 ? 0 : cb) * a.v.max_blocks : nullptr;
     auto fetch = [&](int t) -> int {
@@ -592,7 +585,7 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& c, __nv_bfloat162 m
 // warps would stall on instruction fetches (a tile's boxes unrolled: 2.3 times the time).  Converter
 // thread ct takes piece ct & 3 of rows ct >> 2 and (ct >> 2) + 32 of every slab.  False (the same in
 // every converter thread) if the wait failed or the kernel is aborting.
-template <int kSlabs, bool kHoles>
+template <int kSlabs>
 __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, const TcBox& bx, uint64_t* raw,
                                                uint32_t parity, uint32_t done, volatile int* abort_flag, int ct,
                                                int bar_id) {
@@ -604,8 +597,7 @@ __device__ __forceinline__ bool tc_convert_box(uint8_t* buf, int codes_off, cons
   const __nv_bfloat162 m1 = e8m0_bf162(buf[rb + 32]);
   const uint4* src = reinterpret_cast<const uint4*>(buf + codes_off) + ct;
   uint4 c0 = src[0], c1 = src[kTcConvThreads];
-  const bool in0 = rb < bx.valid && !(kHoles && rb >= bx.h0 && rb < bx.h1);
-  const bool in1 = rb + 32 < bx.valid && !(kHoles && rb + 32 >= bx.h0 && rb + 32 < bx.h1);
+  const bool in0 = bx.sees(rb), in1 = bx.sees(rb + 32);
   uint8_t* dst = buf + rb * 128;   // (rb + 32) & 7 == rb & 7
   const int o0 = ((2 * pc) ^ (rb & 7)) << 4, o1 = ((2 * pc + 1) ^ (rb & 7)) << 4;
 #pragma unroll 1
@@ -653,15 +645,15 @@ __device__ bool tc_convert(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       const uint32_t par = g & 1u;
       if (grp == 0) {
         const TcBox all{64, 0, 0};
-        ok = tc_convert_box<kTcKSlabsA, false>(smem + kTcOffK, kTcFp8OffA, all, &bars->kraw[0], par,
-                                               lbar(&bars->k_full[0]), abort_flag, ct, 3) &&
-             tc_convert_box<kTcKSlabsB, false>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, all, &bars->kraw[1],
-                                               par, lbar(&bars->k_full[1]), abort_flag, ct, 3);
+        ok = tc_convert_box<kTcKSlabsA>(smem + kTcOffK, kTcFp8OffA, all, &bars->kraw[0], par, lbar(&bars->k_full[0]),
+                                        abort_flag, ct, 3) &&
+             tc_convert_box<kTcKSlabsB>(smem + kTcOffK + kTcKSlabsA * kTcSlab, kTcFp8OffB, all, &bars->kraw[1], par,
+                                        lbar(&bars->k_full[1]), abort_flag, ct, 3);
       } else {
         for (int h = 0; ok && h < 2; ++h) {
           const TcBox bx = tc_box<Rows::kHoles>(map, sg.tok_begin + i * kTcTile + 64 * h, sg.tok_end);
-          ok = tc_convert_box<4, Rows::kHoles>(smem + kTcOffV + h * kTcVBox, kTcFp8OffV, bx, &bars->vraw[h], par,
-                                               lbar(&bars->v_full[h]), abort_flag, ct, 4);
+          ok = tc_convert_box<4>(smem + kTcOffV + h * kTcVBox, kTcFp8OffV, bx, &bars->vraw[h], par,
+                                 lbar(&bars->v_full[h]), abort_flag, ct, 4);
         }
       }
     }
@@ -953,15 +945,14 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
     // every warp, so the second half's warps arrive for it too, without waiting for their own half
     // (but for the first one's: no arrival for tile g before PV(g-1) has taken all of tile g-1).
     // Between segments the epilogue waits for more (all of PV), reads O and stages it through the
-    // P buffer; the barrier then lets every warp write P, and both CTAs learn that O may be overwritten.
+    // P buffer; the barrier then lets every warp write P, and PV (the even CTA) learns that O may be overwritten.
     if (i == 0 && k > 0) {
       if (!epilogue(k - 1, red + (j ^ 1) * 256)) return leave(2, n_tiles - i - 1);
       tc_fence_before();
       named_bar_sync(1, 256);
       if (lane == 0) {
         fence_release_smem_to_cluster();
-        mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 0));
-        mbar_arrive_relaxed(mapa_shared(smem_u32(&bars->o_free), 1));
+        mbar_arrive_relaxed(lbar(&bars->o_free));
       }
     } else if (g >= 1 && !wait(&bars->p_empty[0], g - 1, 0x32)) {
       return leave(0, n_tiles - i - 1);

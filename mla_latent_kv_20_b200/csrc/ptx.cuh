@@ -44,14 +44,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Arrive on the barrier at the same shared-memory offset in CTA `cta_rank` of this cluster.
-__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t cta_rank) {
-  asm volatile(
-      "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, %1;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n}\n" ::"r"(smem_u32(bar)),
-      "r"(cta_rank)
-      : "memory");
-}
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -124,15 +116,6 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
-// 2-D tiled load global -> this CTA's shared memory, completion counted on `bar` (bytes).
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y)
-      : "memory");
-}
-
 // 1-D tiled load into this CTA's shared memory, completion counted on a CTA-local barrier.
 __device__ __forceinline__ void tma_load_1d(void* dst, const CUtensorMap* m, uint64_t* bar, int x) {
   asm volatile(
@@ -264,11 +247,6 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t local_addr, uint32_t ra
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local_addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void mbar_arrive_expect_tx_addr(uint32_t bar_cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster_addr),
-               "r"(bytes)
-               : "memory");
-}
 // Count-only arrivals (relaxed): for producers whose data is delivered by TMA complete_tx, so no
 // prior memory operation of the arriving thread needs to be ordered before the arrival.
 __device__ __forceinline__ void mbar_arrive_expect_tx_relaxed(uint32_t bar_cluster_addr, uint32_t bytes) {
@@ -278,9 +256,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_relaxed(uint32_t bar_clust
 }
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar_cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_addr(uint32_t bar_cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
 // Orders this thread's prior writes to its own CTA's shared memory before its subsequent
 // cluster-scope operations (a relaxed mbarrier arrival): the release half of a release arrival,
@@ -296,8 +271,6 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
-// Arrive without waiting (a producer side of a named barrier; its earlier shared-memory writes
-// are visible to the threads that wait on the barrier with bar.sync).
 // Named barrier that also reduces a predicate: every participating thread gets the AND of all of
 // theirs (one outcome for a group of warps that must take the same branch).
 __device__ __forceinline__ bool named_bar_red_and(uint32_t id, uint32_t nthreads, bool pred) {
@@ -309,19 +282,10 @@ __device__ __forceinline__ bool named_bar_red_and(uint32_t id, uint32_t nthreads
       : "memory");
   return r != 0;
 }
+// Arrive without waiting (a producer side of a named barrier; its earlier shared-memory writes
+// are visible to the threads that wait on the barrier with bar.sync).
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// 2-D tiled load into this CTA's shared memory whose completion is counted on an mbarrier that
-// may live in the peer CTA of the pair (bar_cluster_addr from mapa_shared).  No multicast.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar_cluster_addr, int x,
-                                                 int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster_addr), "r"(x), "r"(y)
-      : "memory");
 }
 
 // ---------------------------------------------------------------------------------- tcgen05, CTA pair
