@@ -132,7 +132,8 @@ mla_status mla_cache_append_fp8(const mla_bf16* c_new, const mla_bf16* kr_new, c
  * position the number of tokens before it.
  *   pos [n_tokens] int32, >= 0      slots [n_tokens] int32, in [0, capacity)
  * slots == NULL is MLA_ERR_INVALID_ARG (unless n_tokens == 0); a position or slot outside its range
- * skips the row and sets MLA_DEVERR_POS_RANGE.
+ * skips the row and sets MLA_DEVERR_POS_RANGE.  No two tokens of a call may name the same slot of a
+ * sequence (the row would be a mixture of theirs).
  */
 mla_status mla_cache_append_at(const mla_bf16* c_new, const mla_bf16* kr_new, const int32_t* seq_ids,
                                const int32_t* pos, const int32_t* slots, mla_bf16* cache,
@@ -212,14 +213,18 @@ size_t mla_decode_workspace_size(int32_t batch, int32_t max_seq_len, int32_t num
  * Split-KV flash decoding over P work ranges of 128-token tiles (T tiles in the batch, the last
  * tile of a sequence ragged), planned on the device from seq_lens: when every non-empty sequence
  * has at least T/P tiles, sequence b gets floor(P tiles_b / T) ranges that split its tiles evenly
- * (per-sequence plan); otherwise the tiles of the batch are laid end to end and range p takes
- * [floor(pT/P), floor((p+1)T/P)) (balanced plan), so a range may span several sequences and a
- * sequence several ranges.  Each part of a sequence a range covers keeps a running max m and sum
+ * (per-sequence plan); otherwise the tiles of the batch are laid end to end and cut into P ranges of
+ * equal cost, where the start of a sequence counts as two tiles (balanced plan), so a range may span
+ * several sequences and a sequence several ranges.  Each part of a sequence a range covers keeps a running max m and sum
  * l (online softmax); a sequence covered by one range is finished by the decode kernel, the
  * others' unnormalised partials are merged by a combine in ascending range order:
  *     out_lat[b, h, :] = sum_r e^{m_r - M} O_r / sum_r e^{m_r - M} l_r,   M = max_r m_r
  *     lse[b, h]        = M + log(sum_r e^{m_r - M} l_r)                    (natural log)
- * The ranges depend only on seq_lens and P.
+ * The ranges depend only on seq_lens and P, and so do the bits of the result.
+ * Precision: products of bf16 values are exact, scores, softmax statistics and sums are fp32; the
+ * weights e^{s - m} are rounded to bf16 for the product with c (relative error at most 2^-8 each, l sums
+ * the unrounded ones), the latent output is rounded to bf16 once.  Against 64 bits, out_lat is off by
+ * 0.0019-0.0025 of its 2-norm on random rows, of which the rounding of the output alone makes 0.0017.
  *   q_full   [batch, 128, 576] bf16     cache / block_table per desc     seq_lens [batch] int32
  *   softmax_scale: e.g. 1/sqrt(192)     num_splits: work ranges P, 0 = auto, else forced
  *   workspace: >= mla_decode_workspace_size(batch, desc.max_seq_len or capacity, num_splits) bytes,
@@ -273,6 +278,7 @@ mla_status mla_prefill_attn(const mla_bf16* q_full, const mla_bf16* cache, const
  *   workspace >= mla_decode_workspace_size(rows, mla_window_span(capacity, window, sinks), num_splits)
  *   bytes, capacity = max_seq_len or max_blocks_per_seq * 64 (the size for the full capacity also serves)
  * Work ranges are planned over the visible boxes only; results do not depend on the cache layout.
+ * Precision as in (3): the weights are rounded to bf16 for the product with c, everything else is fp32.
  */
 mla_status mla_decode_attn_window(const mla_bf16* q_full, const mla_bf16* cache, const int32_t* block_table,
                                   const int32_t* seq_lens, mla_cache_desc desc, int32_t batch, int32_t window,
@@ -298,11 +304,14 @@ int32_t mla_window_span(int32_t max_seq_len, int32_t window, int32_t sinks);
  *         weights[b * capacity + t] = decay * prev[b * capacity + t]
  *                                   + sum_i sum_h exp(softmax_scale * q_full[i, h] . row(b, t) - lse[i, h])
  * with lse as the attention call over the same rows, queries and scale wrote it: the terms of one row
- * then sum to 128 over its tokens.  Elements at t >= seq_lens[b] are left as they were.
+ * then sum to 128 over its tokens.  That is the attention of (3), (3-fp8) or (7): a windowed call's lse
+ * belongs to the visible tokens only, and the hidden ones would be given weights they never had (it
+ * serves where every row sees all its tokens, L <= sinks + window).  Elements at t >= seq_lens[b] are left as they were.
  *   mla_attn_weights(_fp8), after mla_decode_attn(_fp8): one row per sequence, i = b.
  *   mla_prefill_attn_weights, after mla_prefill_attn: the rows of sequence b are q_start[b] <= i <
  *     q_start[b + 1], and row i counts for t < q_len[i].  A sequence without rows: decay * prev.
- * Products in fp32 (exact for bf16), sums and exponentials in fp32; the same bits on every call.
+ * Products in fp32 (exact for bf16), sums and exponentials (2^x by the hardware's approximation, within
+ * about 2^-22) in fp32; the same bits on every call.
  *   q_full [rows, 128, 576] bf16   lse [rows, 128] fp32 (a head whose lse is -inf adds nothing)
  *   prev   [batch, capacity] fp32, or NULL (taken as 0); weights may be prev
  *   decay  >= 0, finite            weights [batch, capacity] fp32, capacity = max_seq_len or
@@ -348,10 +357,12 @@ mla_status mla_prefill_attn_weights(const mla_bf16* q_full, const mla_bf16* cach
  *   workspace >= mla_evict_workspace_size(batch, keep) bytes, 16-byte aligned
  * In place: cache_out == cache (FP8: scales_out == scales too), page size and, contiguous, max_seq_len
  * of the two descriptors equal; slots of cache_out must then be the same sequence's own slots at the
- * same place, or pages that no sequence's tokens are read from.  Otherwise the two buffers must not meet
- * (MLA_ERR_INVALID_ARG).  weights_out may be weights where the capacities are equal, lens_out may be
- * seq_lens; no other outputs may overlap inputs.  A length outside [0, capacity] is clamped
- * (MLA_DEVERR_SEQLEN_RANGE); a row whose block id is out of range is skipped (MLA_DEVERR_BLOCK_RANGE).
+ * same place, or pages that no sequence's tokens are read from: a page that two sequences share (a
+ * common prefix) is not a sequence's own, and such sequences are evicted into other pages.  Otherwise
+ * the two buffers must not meet (MLA_ERR_INVALID_ARG).  weights_out may be weights where the capacities
+ * are equal, lens_out may be seq_lens; no other outputs may overlap inputs.  A length outside
+ * [0, capacity] is clamped (MLA_DEVERR_SEQLEN_RANGE); a row whose block id is out of range is skipped
+ * (MLA_DEVERR_BLOCK_RANGE).
  */
 size_t mla_evict_workspace_size(int32_t batch, int32_t keep);
 mla_status mla_cache_evict(const mla_bf16* cache, const int32_t* block_table, const int32_t* seq_lens,

@@ -203,9 +203,14 @@ mla_status launch_attn(const mla_bf16* q_full, const void* cache, const int32_t*
   if (ls != MLA_OK) return ls;
   if (P == 1 && rows <= mla::kTcOwnEmptyRows) return MLA_OK;   // one range covers every row
   auto* out = reinterpret_cast<__nv_bfloat16*>(out_lat);
-  if (rows <= 8)   // few rows, perhaps of many partials
+  // Few rows, perhaps of many partials: a block per head, else one per four heads.  The call with the one / the other,
+  // 262144 tokens of one range per SM pair in 1 row 104 / 126 us, 4 rows 91 / 96, 8 89.1 / 91.5, 9 88.4 / 91.1,
+  // 12 90.0 / 89.7, 16 94.1 / 92.8, 32 97.6 / 92.4.
+  if (rows <= 8)
     return launch_chained(mla::combine_kernel<1, false>, dim3(rows, mla::kHeads), dim3(128), 0, s, a.ws, P, rows, out,
                           lse);
+  // More rows than ranges: a block per range.  By range / by row: 75 x 2048 77.8 / 75.5 us, 200 x 1000 94.9 / 94.1, 300 x 300
+  // 76 / 80, 512 x 256 89 / 101, 1000 x 0..500 150 / 177, 1024 chunk rows 255 / 279.
   if (rows <= P)
     return launch_chained(mla::combine_kernel<4, false>, dim3(rows, mla::kHeads / 4), dim3(128), 0, s, a.ws, P, rows,
                           out, lse);

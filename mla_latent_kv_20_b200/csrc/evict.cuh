@@ -9,7 +9,7 @@
 // histogram of the keys that share the digits found so far, done early when all of them are kept), then
 // numbers the kept tokens in order.  A cluster of CTAs shares a long sequence: each holds the order keys of
 // its slice in shared memory, and the histograms are summed through distributed shared memory.  It is bound
-// by the latency of its steps: 3-6 us beside the launch for up to 8192 tokens a CTA.
+// by the latency of its steps: 8-12 us for 128 sequences of 1024..8192 tokens, a CTA each.
 //
 // The move is a copy bound by HBM, the rows' bytes read once and written once: 128 x 1024 rows (302 MB) in
 // 53 us, 5.7 TB/s, 0.88 of the measured copy rate.  Few rows are moved by the selection kernel itself.
@@ -74,8 +74,7 @@ struct EvictCache {
 };
 
 // What the move writes beside the rows: the weights at their new slots, zeros in the slots that the
-// eviction freed (up to the old length), and the new lengths.
-// me of all threads.
+// eviction freed (up to the old length), and the new lengths.  By thread `me` of `all`.
 __device__ __forceinline__ void ev_write_weights(const EvictWorkspace& ws, int b, int L, int keep, int capacity_out,
                                                  float* weights_out, int32_t* lens_out, int64_t me, int64_t all) {
   const int n = min(L, keep);
@@ -93,9 +92,16 @@ struct EvictMove {
   int32_t* lens_out;
 };
 // At most this many kept tokens are moved by the selection itself (one CTA of the cluster does it): one launch
-// instead of two, which is what a short call costs.  300 tokens to 128: 8.3 us a call, two launches 1.9 more;
-// 128 x 1000..4000 to 64: 12.2 instead of 14.7.  Its reads are all in flight at once; more rows are better spread
-// over the device by a launch of their own.
+// instead of two, which is what a short call costs.  Its reads are all in flight at once, 18 pieces of 16 bytes
+// a thread for 128 bf16 rows, which is what its registers hold.  Calls over cold inputs, alone, one launch / two:
+//   sequences of 1000 tokens, bf16:   to 16          to 64          to 128
+//     1                               14.3 / 15.4    15.0 / 15.4    16.3 / 15.4   (to 129..512, two: 15.4-15.6)
+//     32                              14.7 / 15.4    15.7 / 17.4    16.8 / 17.4
+//     148                             15.0 / 17.4    17.1 / 19.4    20.9 / 23.0
+//     512                             39.3 / 33.8    45.3 / 44.0    53.1 / 55.3
+//     1024                            65.1 / 54.3    76.0 / 72.7    90.7 / 95.2
+// and FP8, half the bytes: to 128 15.0 / 15.4, 14.8 / 17.4, 16.8 / 19.4, 43.8 / 46.1, 74.0 / 76.8 us.  (From the second
+// wave of blocks on, few rows of many sequences would take two launches: left, for such a call is rare.)
 constexpr int kEvMoveRows = 128;
 
 // One CTA moves the first n <= kEvMoveRows slots' rows of sequence b: reads them all, waits for all threads,

@@ -747,7 +747,9 @@ mla_status launch_evict(const void* cache, const uint8_t* scales, const int32_t*
     return MLA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < mla::ev_ws_bytes(batch, keep))
     return MLA_ERR_WORKSPACE;
-  // CTAs per sequence: one per 4096 tokens of capacity, while the clusters together fit the SMs.
+  // CTAs per sequence: one per 4096 tokens of capacity, while the clusters together fit the SMs.  To 64 tokens, bf16,
+  // cold inputs, alone, so / always one CTA: 1 x 8192 21.4 / 21.9, 16384 22.3 / 29.7, 32768 24.9 / 68, 131072 35 / 348 us,
+  // 8 x 32768 25.0 / 68; one per 2048 tokens 20.5, 21.4, 25.0, 35.3, 24.9, one per 8192 22.0, 26.1, 28.6, 35.0, 28.7.
   int C = 1;
   while (C < mla::kEvMaxCluster && capacity / C > 4096 && 2 * C * batch <= device_sm_count()) C *= 2;
   const mla::EvictWorkspace ws = mla::ev_carve(workspace, batch, keep);
