@@ -314,12 +314,12 @@ TRAFFIC_SOURCES = ("csrc/decode_tc.cuh", "csrc/decode_common.cuh", "csrc/ptx.cuh
                    "csrc/decode_launch.cuh")
 MEASURED_TRAFFIC = {   # workload[@ranges] -> {"bytes": int, "sha256": str, "profile": str}
     "b128_u1024_8192_paged": {
-        "bytes": 692737536 + 26730752 + 36341760,
-        "sha256": "718942ef98c3b9e43adddeb17c4c750231abb198ff23025d2da1dbaf94bc3095",
+        "bytes": 692698112 + 26379776 + 36340992,
+        "sha256": "cadeeae45057d75d2ca6cfd90d678e8b5da342c6402eacd9f079ab798e5daf5f",
         "profile": "profiles/decode_tc_b128_u1024_8192_paged.md (decode + combine, ncu cache flush per kernel)"},
     "b32_l4096": {
-        "bytes": 155795968 + 3335424 + 16865024,
-        "sha256": "718942ef98c3b9e43adddeb17c4c750231abb198ff23025d2da1dbaf94bc3095",
+        "bytes": 155832832 + 2929152 + 16864000,
+        "sha256": "cadeeae45057d75d2ca6cfd90d678e8b5da342c6402eacd9f079ab798e5daf5f",
         "profile": "profiles/decode_tc_b32_l4096.md (decode + combine, ncu cache flush per kernel)"},
 }
 
