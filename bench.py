@@ -315,11 +315,11 @@ TRAFFIC_SOURCES = ("csrc/decode_tc.cuh", "csrc/decode_common.cuh", "csrc/ptx.cuh
 MEASURED_TRAFFIC = {   # workload[@ranges] -> {"bytes": int, "sha256": str, "profile": str}
     "b128_u1024_8192_paged": {
         "bytes": 692698112 + 26379776 + 36340992,
-        "sha256": "cadeeae45057d75d2ca6cfd90d678e8b5da342c6402eacd9f079ab798e5daf5f",
+        "sha256": "53d2d2dc6e709c48148cd88d7eecfb10640eb23750a0a363f154958c9f8ab43c",
         "profile": "profiles/decode_tc_b128_u1024_8192_paged.md (decode + combine, ncu cache flush per kernel)"},
     "b32_l4096": {
         "bytes": 155832832 + 2929152 + 16864000,
-        "sha256": "cadeeae45057d75d2ca6cfd90d678e8b5da342c6402eacd9f079ab798e5daf5f",
+        "sha256": "53d2d2dc6e709c48148cd88d7eecfb10640eb23750a0a363f154958c9f8ab43c",
         "profile": "profiles/decode_tc_b32_l4096.md (decode + combine, ncu cache flush per kernel)"},
 }
 

@@ -201,9 +201,9 @@ struct SegmentCursor {
 // kByRange: block x < P takes the row whose first piece range x holds, if it is split (fewer rows are split
 // than there are ranges), looked up in the plan table, and the blocks from P on look over 32 rows each
 // for empty ones; otherwise block x takes row x.  An empty row is written by the blocks y of its x, kCols
-// heads each (one block a row: 4000 rows of nothing 286 us, 127 now).  A warp covers 128 kCols latent columns of a head (a lane kCols pieces of four), a block
-// of four warps kCols heads: kCols = 4 where there are rows enough to fill the device, 1 where few rows
-// may have many partials each.  8 / kCols partials are in flight at a time; their m and l are read by
+// heads each (one block a row: 4000 rows of nothing 286 us, 127 now).  A warp covers 128 kCols latent
+// columns of a head (a lane kCols pieces of four), a block of four warps kCols heads: kCols = 4 where there
+// are rows enough to fill the device, 1 where few rows may have many partials each.  8 / kCols partials are in flight at a time; their m and l are read by
 // lane i for the row's i-th range, 32 ranges at once.
 template <int kCols, bool kByRange>
 __global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int P, int B, __nv_bfloat16* __restrict__ out_lat,

@@ -943,11 +943,13 @@ __device__ void tc_softmax(const DecodeTcArgs& a, const TcPlan& plan, int pair, 
       pk[e] = *reinterpret_cast<uint32_t*>(&h2);
     }
     // A half of the P buffer is free once PV(g-1) has read it.  By parity this is unambiguous: both halves'
-    // warps waited in tile g-1 for their half of PV(g-2), so p_empty has completed g-1 or g phases.  PV of the first half needs O corrected by
-    // every warp, so the second half's warps arrive for it too, without waiting for their own half
-    // (but for the first one's: no arrival for tile g before PV(g-1) has taken all of tile g-1).
-    // Between segments the epilogue waits for more (all of PV), reads O and stages it through the
-    // P buffer; the barrier then lets every warp write P, and PV (the even CTA) learns that O may be overwritten.
+    // warps waited in tile g-1 for their half of PV(g-2), so p_empty has completed g-1 or g phases.  PV of
+    // the first half needs O corrected by every warp, so the second half's warps arrive for it too, without
+    // waiting for their own half (but for the first one's: no arrival for tile g before PV(g-1) has taken
+    // all of tile g-1).
+    // Between segments the epilogue waits for more (all of PV), reads O and stages it through the P
+    // buffer; the barrier then lets every warp write P, and PV (the even CTA) learns that O may be
+    // overwritten.
     if (i == 0 && k > 0) {
       if (!epilogue(k - 1, red + (j ^ 1) * 256)) return leave(2, n_tiles - i - 1);
       tc_fence_before();
